@@ -23,6 +23,7 @@
 #include "fa_bwd_pair.cuh"
 #include "fa_bwd_q128.cuh"
 #include "fa_decode.cuh"
+#include "fa_kv4.cuh"
 
 namespace {
 
@@ -371,6 +372,65 @@ void launch_merge(const float *o_part, const float *lse_part, void *o, float *ls
   if (d == 64) fa::fa_merge_kernel<64><<<grid, 256, 0, s>>>(o_part, lse_part, ob, lse, S, rows);
   else if (d == 128) fa::fa_merge_kernel<128><<<grid, 256, 0, s>>>(o_part, lse_part, ob, lse, S, rows);
   else fa::fa_merge_kernel<256><<<grid, 256, 0, s>>>(o_part, lse_part, ob, lse, S, rows);
+}
+
+// ---- the 4-bit cache
+
+int check_kv4_sizes(int B, int Hkv, int cap, int d) {
+  if (B < 1 || Hkv < 1 || cap < 1) return FA_ERR_INVALID_ARG;
+  if (d != 64 && d != 128 && d != 256) return FA_ERR_UNSUPPORTED;
+  if (cap % fa::kKV4CapMultiple != 0 || cap > (1 << 30) || static_cast<long long>(B) * Hkv * cap >= (1ll << 31))
+    return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+int check_kv4_decode(int B, int Hq, int Hkv, int Nq, int cap, int d, float scale) {
+  if (B < 1 || Hq < 1 || Hkv < 1 || Nq < 1) return FA_ERR_INVALID_ARG;
+  if (!(scale > 0.f) || !std::isfinite(scale)) return FA_ERR_INVALID_ARG;
+  int rc = check_kv4_sizes(B, Hkv, cap, d);
+  if (rc != FA_OK) return rc;
+  if (Hq % Hkv != 0) return FA_ERR_GQA;
+  // grid.y holds (batch, K/V head)
+  if (static_cast<long long>(Hq / Hkv) * Nq > 128 || static_cast<long long>(B) * Hkv > 65535 ||
+      static_cast<long long>(B) * Hq * Nq >= (1ll << 31))
+    return FA_ERR_UNSUPPORTED;
+  return FA_OK;
+}
+
+// The two arguments that change the scores: a cap (0: none) and a slope per query head
+// (nullptr: none).
+int check_score_args(float softcap, const float *slopes) {
+  if (!(softcap >= 0.f) || !std::isfinite(softcap)) return FA_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(slopes) & 3u) return FA_ERR_ALIGN;
+  return FA_OK;
+}
+
+// 8-row tiles of query rows that one CTA takes.
+int kv4_row_tiles(int R, int d) { return R > 8 && d != 256 ? 2 : 1; }
+
+// Writes (store) or reads n tokens of the cache.
+int run_kv4_copy(bool store, fa::KV4Params &p, int d, cudaStream_t s) {
+  const long long threads = 2ll * p.B * p.Hkv * p.n * (d / 8);
+  const long long grid = (threads + 255) / 256;
+  if (grid >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  const unsigned gr = static_cast<unsigned>(grid);
+  if (store) {
+    if (d == 64) fa::fa_kv4_write_kernel<64><<<gr, 256, 0, s>>>(p);
+    else if (d == 128) fa::fa_kv4_write_kernel<128><<<gr, 256, 0, s>>>(p);
+    else fa::fa_kv4_write_kernel<256><<<gr, 256, 0, s>>>(p);
+  } else {
+    if (d == 64) fa::fa_kv4_read_kernel<64><<<gr, 256, 0, s>>>(p);
+    else if (d == 128) fa::fa_kv4_read_kernel<128><<<gr, 256, 0, s>>>(p);
+    else fa::fa_kv4_read_kernel<256><<<gr, 256, 0, s>>>(p);
+  }
+  return cuda_ok(cudaGetLastError(), store ? "fa_kv4_write launch" : "fa_kv4_read launch") ? FA_OK : FA_ERR_CUDA;
+}
+
+template <int D, int NT>
+void launch_kv4(const fa::KV4DecodeParams &p, cudaStream_t s) {
+  const dim3 grid(static_cast<unsigned>(p.splits), static_cast<unsigned>(p.B) * p.Hkv,
+                  static_cast<unsigned>((p.R + 8 * NT - 1) / (8 * NT)));
+  fa::fa_decode_kv4_kernel<D, NT><<<grid, fa::kKV4Warps * 32, 0, s>>>(p);
 }
 
 // Launches the forward kernel for d (maps and parameters prepared by the caller).
@@ -981,6 +1041,141 @@ int fa_decode(const void *q, const void *k, const void *v, void *o, float *lse, 
   timer_stop(2, tslot, s);
   if (num_splits > 1) launch_merge(p.o_part, p.lse_part, o, lse, num_splits, static_cast<long long>(rows), d, s);
   return cuda_ok(cudaGetLastError(), "fa_decode launch") ? FA_OK : FA_ERR_CUDA;
+}
+
+int fa_kv4_write(const void *k, const void *v, void *k_codes, void *k_params, void *v_codes, void *v_params,
+                 const int *start, const int *counts, int B, int Hkv, int n, int cap, int d, void *stream) {
+  if (!k || !v || !k_codes || !k_params || !v_codes || !v_params || n < 0) return FA_ERR_INVALID_ARG;
+  int rc = check_kv4_sizes(B, Hkv, cap, d);
+  if (rc != FA_OK) return rc;
+  if (n > cap) return FA_ERR_UNSUPPORTED;
+  const void *ptrs[] = {k, v, k_codes, k_params, v_codes, v_params};
+  for (const void *ptr : ptrs)
+    if (!aligned16(ptr)) return FA_ERR_ALIGN;
+  if ((reinterpret_cast<uintptr_t>(start) & 3u) || (reinterpret_cast<uintptr_t>(counts) & 3u)) return FA_ERR_ALIGN;
+  if (!device_ready()) return FA_ERR_CUDA;
+  if (n == 0) return FA_OK;
+  fa::KV4Params p{};
+  p.kc = static_cast<uint8_t *>(k_codes);
+  p.vc = static_cast<uint8_t *>(v_codes);
+  p.kp = static_cast<__half *>(k_params);
+  p.vp = static_cast<__half *>(v_params);
+  p.k = static_cast<__nv_bfloat16 *>(const_cast<void *>(k));
+  p.v = static_cast<__nv_bfloat16 *>(const_cast<void *>(v));
+  p.start = start;
+  p.counts = counts;
+  p.B = B;
+  p.Hkv = Hkv;
+  p.n = n;
+  p.cap = cap;
+  return run_kv4_copy(true, p, d, static_cast<cudaStream_t>(stream));
+}
+
+int fa_kv4_read(const void *k_codes, const void *k_params, const void *v_codes, const void *v_params, void *k,
+                void *v, const int *start, int B, int Hkv, int n, int cap, int d, void *stream) {
+  if (!k || !v || !k_codes || !k_params || !v_codes || !v_params || n < 0) return FA_ERR_INVALID_ARG;
+  int rc = check_kv4_sizes(B, Hkv, cap, d);
+  if (rc != FA_OK) return rc;
+  if (n > cap) return FA_ERR_UNSUPPORTED;
+  const void *ptrs[] = {k, v, k_codes, k_params, v_codes, v_params};
+  for (const void *ptr : ptrs)
+    if (!aligned16(ptr)) return FA_ERR_ALIGN;
+  if (reinterpret_cast<uintptr_t>(start) & 3u) return FA_ERR_ALIGN;
+  if (!device_ready()) return FA_ERR_CUDA;
+  if (n == 0) return FA_OK;
+  fa::KV4Params p{};
+  p.kc = static_cast<uint8_t *>(const_cast<void *>(k_codes));
+  p.vc = static_cast<uint8_t *>(const_cast<void *>(v_codes));
+  p.kp = static_cast<__half *>(const_cast<void *>(k_params));
+  p.vp = static_cast<__half *>(const_cast<void *>(v_params));
+  p.k = static_cast<__nv_bfloat16 *>(k);
+  p.v = static_cast<__nv_bfloat16 *>(v);
+  p.start = start;
+  p.B = B;
+  p.Hkv = Hkv;
+  p.n = n;
+  p.cap = cap;
+  return run_kv4_copy(false, p, d, static_cast<cudaStream_t>(stream));
+}
+
+int fa_decode_kv4_num_splits(int B, int Hq, int Hkv, int Nq, int cap, int d) {
+  if (check_kv4_decode(B, Hq, Hkv, Nq, cap, d, 1.0f) != FA_OK) return 0;
+  int sms = 148, dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) {
+    (void)cudaGetLastError();
+    sms = 148;
+  }
+  const int R = Hq / Hkv * Nq, rows = 8 * kv4_row_tiles(R, d);
+  const long long units = static_cast<long long>(B) * Hkv * ((R + rows - 1) / rows);
+  long long s = units >= 2 * sms ? 1 : 2 * sms / units;
+  const long long most = (cap + fa::kKV4Warps * fa::kKV4Keys - 1) / (fa::kKV4Warps * fa::kKV4Keys);
+  if (s > most) s = most;
+  if (s > kMaxDecodeSplits) s = kMaxDecodeSplits;
+  return static_cast<int>(s < 1 ? 1 : s);
+}
+
+size_t fa_decode_kv4_workspace_bytes(int B, int Hq, int Hkv, int Nq, int cap, int d, int num_splits) {
+  if (check_kv4_decode(B, Hq, Hkv, Nq, cap, d, 1.0f) != FA_OK) return 0;
+  if (num_splits < 1 || num_splits > kMaxDecodeSplits) return 0;
+  return decode_workspace(B, Hq, Nq, d, num_splits);
+}
+
+int fa_decode_kv4(const void *q, const void *k_codes, const void *k_params, const void *v_codes, const void *v_params,
+                  void *o, float *lse, const int *seqlens_k, const float *alibi_slopes, void *workspace,
+                  size_t workspace_bytes, int B, int Hq, int Hkv, int Nq, int cap, int d, int causal, int num_splits,
+                  float softcap, float scale, void *stream) {
+  if (!q || !k_codes || !k_params || !v_codes || !v_params || !o || !lse) return FA_ERR_INVALID_ARG;
+  if (causal != 0 && causal != 1) return FA_ERR_INVALID_ARG;
+  if (num_splits < 1 || num_splits > kMaxDecodeSplits) return FA_ERR_INVALID_ARG;
+  int rc = check_kv4_decode(B, Hq, Hkv, Nq, cap, d, scale);
+  if (rc == FA_OK) rc = check_score_args(softcap, alibi_slopes);
+  if (rc != FA_OK) return rc;
+  const size_t need = decode_workspace(B, Hq, Nq, d, num_splits);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return FA_ERR_WORKSPACE;
+  const void *ptrs[] = {q, k_codes, k_params, v_codes, v_params, o, lse};
+  for (const void *ptr : ptrs)
+    if (!aligned16(ptr)) return FA_ERR_ALIGN;
+  if ((need > 0 && !aligned16(workspace)) || (reinterpret_cast<uintptr_t>(seqlens_k) & 3u)) return FA_ERR_ALIGN;
+  if (!device_ready()) return FA_ERR_CUDA;
+
+  const size_t rows = static_cast<size_t>(B) * Hq * Nq;
+  fa::KV4DecodeParams p{};
+  p.q = static_cast<const __nv_bfloat16 *>(q);
+  p.kc = static_cast<const uint8_t *>(k_codes);
+  p.vc = static_cast<const uint8_t *>(v_codes);
+  p.kp = static_cast<const __half *>(k_params);
+  p.vp = static_cast<const __half *>(v_params);
+  p.lens = seqlens_k;
+  p.slopes = alibi_slopes;
+  p.o = static_cast<__nv_bfloat16 *>(o);
+  p.lse = lse;
+  if (num_splits > 1) {
+    p.o_part = static_cast<float *>(workspace);
+    p.lse_part = reinterpret_cast<float *>(static_cast<char *>(workspace) +
+                                           fa::pad256(static_cast<size_t>(num_splits) * rows * d * 4));
+  }
+  p.B = B;
+  p.Hkv = Hkv;
+  p.Nq = Nq;
+  p.R = Hq / Hkv * Nq;
+  p.cap = cap;
+  p.splits = num_splits;
+  const int per = (cap + num_splits - 1) / num_splits;
+  p.chunk = (per + fa::kKV4CapMultiple - 1) / fa::kKV4CapMultiple * fa::kKV4CapMultiple;
+  p.causal = causal;
+  p.scale = scale;
+  p.sl2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  p.softcap = softcap;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const int tslot = timer_start(2, s);
+  const bool two = kv4_row_tiles(p.R, d) == 2;
+  if (d == 64) two ? launch_kv4<64, 2>(p, s) : launch_kv4<64, 1>(p, s);
+  else if (d == 128) two ? launch_kv4<128, 2>(p, s) : launch_kv4<128, 1>(p, s);
+  else launch_kv4<256, 1>(p, s);
+  timer_stop(2, tslot, s);
+  if (num_splits > 1) launch_merge(p.o_part, p.lse_part, o, lse, num_splits, static_cast<long long>(rows), d, s);
+  return cuda_ok(cudaGetLastError(), "fa_decode_kv4 launch") ? FA_OK : FA_ERR_CUDA;
 }
 
 int fa_merge(const float *o_parts, const float *lse_parts, void *o, float *lse, int num_parts, int rows,

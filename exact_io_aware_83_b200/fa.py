@@ -27,6 +27,7 @@ Entry points mirror the C ABI names:
 """
 from __future__ import annotations
 
+import collections
 import ctypes
 import math
 import os
@@ -108,6 +109,17 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.fa_decode.argtypes = [vp, vp, vp, vp, vp, vp, vp, sz, ci, ci, ci, ci, ci, ci, ci, ci,
                                   cf, vp]
         lib.fa_decode.restype = ci
+        lib.fa_kv4_write.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, vp]
+        lib.fa_kv4_write.restype = ci
+        lib.fa_kv4_read.argtypes = [vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, vp]
+        lib.fa_kv4_read.restype = ci
+        lib.fa_decode_kv4.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, ci, ci, ci, ci,
+                                      ci, ci, ci, ci, cf, cf, vp]
+        lib.fa_decode_kv4.restype = ci
+        lib.fa_decode_kv4_num_splits.argtypes = [ci, ci, ci, ci, ci, ci]
+        lib.fa_decode_kv4_num_splits.restype = ci
+        lib.fa_decode_kv4_workspace_bytes.argtypes = [ci, ci, ci, ci, ci, ci, ci]
+        lib.fa_decode_kv4_workspace_bytes.restype = sz
         lib.fa_merge.argtypes = [vp, vp, vp, vp, ci, ci, ci, vp]
         lib.fa_merge.restype = ci
         lib.fa_bwd_noalloc.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp,
@@ -245,6 +257,35 @@ def fa_decode(q, k, v, o, lse, seqlens_k, workspace, workspace_bytes, B, Hq, Hkv
     _check(load().fa_decode(q, k, v, o, lse, seqlens_k, workspace, workspace_bytes, B, Hq, Hkv,
                             Nq, Nk, d, int(causal), int(num_splits), float(scale), stream),
            "fa_decode")
+
+
+def fa_kv4_write(k, v, k_codes, k_params, v_codes, v_params, start, counts, B, Hkv, n, cap, d,
+                 stream) -> None:
+    _check(load().fa_kv4_write(k, v, k_codes, k_params, v_codes, v_params, start, counts, B, Hkv,
+                               n, cap, d, stream), "fa_kv4_write")
+
+
+def fa_kv4_read(k_codes, k_params, v_codes, v_params, k, v, start, B, Hkv, n, cap, d,
+                stream) -> None:
+    _check(load().fa_kv4_read(k_codes, k_params, v_codes, v_params, k, v, start, B, Hkv, n, cap,
+                              d, stream), "fa_kv4_read")
+
+
+def fa_decode_kv4_num_splits(B, Hq, Hkv, Nq, cap, d) -> int:
+    return int(load().fa_decode_kv4_num_splits(B, Hq, Hkv, Nq, cap, d))
+
+
+def fa_decode_kv4_workspace_bytes(B, Hq, Hkv, Nq, cap, d, num_splits) -> int:
+    return int(load().fa_decode_kv4_workspace_bytes(B, Hq, Hkv, Nq, cap, d, num_splits))
+
+
+def fa_decode_kv4(q, k_codes, k_params, v_codes, v_params, o, lse, seqlens_k, alibi_slopes,
+                  workspace, workspace_bytes, B, Hq, Hkv, Nq, cap, d, causal, num_splits, softcap,
+                  scale, stream) -> None:
+    _check(load().fa_decode_kv4(q, k_codes, k_params, v_codes, v_params, o, lse, seqlens_k,
+                                alibi_slopes, workspace, workspace_bytes, B, Hq, Hkv, Nq, cap, d,
+                                int(causal), int(num_splits), float(softcap), float(scale),
+                                stream), "fa_decode_kv4")
 
 
 def fa_merge(o_parts, lse_parts, o, lse, num_parts, rows, d, stream) -> None:
@@ -444,6 +485,152 @@ def decode(q, k, v, seqlens_k=None, causal: bool = False, scale: float | None = 
     fa_decode(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), l.data_ptr(), lens_ptr,
               ws_ptr, ws_bytes, B, Hq, Hkv, Nq, Nk, d, causal, num_splits, scale,
               _stream_handle(q))
+    return o, l
+
+
+#: A key/value cache held in 4 bits (see fa_kv4_write in include/fa.h for the format):
+#: uint8 [B, Hkv, cap, d/2] codes and fp16 [B, Hkv, cap, 2 d/32] params of K and of V.
+KV4Cache = collections.namedtuple("KV4Cache", "k_codes k_params v_codes v_params")
+
+
+def kv4_alloc(B: int, Hkv: int, cap: int, d: int, device="cuda"):
+    """An empty 4-bit cache for `cap` tokens (a multiple of 64).  Its memory is not
+    initialised: only what kv4_write wrote may be read or attended to."""
+    import torch
+    if d not in (64, 128, 256) or cap < 1 or cap % 64 or B < 1 or Hkv < 1:
+        raise ValueError("kv4_alloc needs B, Hkv >= 1, cap a multiple of 64 and d in {64, 128, 256}")
+    codes = lambda: torch.empty((B, Hkv, cap, d // 2), dtype=torch.uint8, device=device)
+    params = lambda: torch.empty((B, Hkv, cap, d // 16), dtype=torch.float16, device=device)
+    return KV4Cache(codes(), params(), codes(), params())
+
+
+def _kv4(cache):
+    """(B, Hkv, cap, d) of a cache, after checking its four tensors."""
+    import torch
+    kc = cache.k_codes
+    if kc.dim() != 4:
+        raise ValueError("cache codes must be [B, Hkv, cap, d/2]")
+    B, Hkv, cap, half = kc.shape
+    d = 2 * half
+    for t, n, dt, last in ((kc, "k_codes", torch.uint8, half),
+                           (cache.k_params, "k_params", torch.float16, d // 16),
+                           (cache.v_codes, "v_codes", torch.uint8, half),
+                           (cache.v_params, "v_params", torch.float16, d // 16)):
+        if (not t.is_cuda or t.dtype != dt or not t.is_contiguous() or t.device != kc.device
+                or tuple(t.shape) != (B, Hkv, cap, last)):
+            raise ValueError(f"{n} must be a contiguous {dt} CUDA tensor [{B}, {Hkv}, {cap}, {last}]")
+    return B, Hkv, cap, d
+
+
+def _int32_vector(t, name, B, device):
+    """Device pointer of an int32 [B] tensor (None stays None)."""
+    import torch
+    if t is None:
+        return None
+    if (not t.is_cuda or t.dtype != torch.int32 or tuple(t.shape) != (B,) or not t.is_contiguous()
+            or t.device != device):
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of B = {B} entries on {device}")
+    return t.data_ptr()
+
+
+def _slopes(alibi_slopes, Hq, device):
+    """Device pointer of the fp32 [Hq] distance slopes (None stays None)."""
+    import torch
+    if alibi_slopes is None:
+        return None
+    if (not alibi_slopes.is_cuda or alibi_slopes.dtype != torch.float32 or alibi_slopes.device != device
+            or tuple(alibi_slopes.shape) != (Hq,) or not alibi_slopes.is_contiguous()):
+        raise ValueError(f"alibi_slopes must be a contiguous fp32 CUDA tensor of Hq = {Hq} entries on {device}")
+    return alibi_slopes.data_ptr()
+
+
+def _same_device(first, *others):
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"all tensors must be on one device ({t.device} is not {first.device})")
+
+
+def _out(t, name, shape, dtype, like):
+    """`t`, checked to be an output tensor of that shape, or a new one."""
+    import torch
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if not t.is_cuda or t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor {list(shape)}")
+    _same_device(like, t)
+    return t
+
+
+def kv4_write(cache, k, v, start=None, counts=None) -> None:
+    """Quantise new tokens k, v [B, Hkv, n, d] bf16 into positions start[b] .. start[b]+n-1 of
+    the cache (int32 [B] on the GPU, or None: 0); with counts (int32 [B]) only the first
+    counts[b] of them.  Positions outside the cache are skipped and reported by
+    fa_device_status as FA_ERR_SEQLENS."""
+    import torch
+    B, Hkv, cap, d = _kv4(cache)
+    for t, n in ((k, "k"), (v, "v")):
+        _need(t, n)
+    if k.dim() != 4 or v.shape != k.shape or tuple(k.shape[:2]) != (B, Hkv) or k.shape[3] != d:
+        raise ValueError(f"expected k and v [{B}, {Hkv}, n, {d}], got {tuple(k.shape)} and {tuple(v.shape)}")
+    _same_device(cache.k_codes, k, v)
+    sp, cp = _int32_vector(start, "start", B, k.device), _int32_vector(counts, "counts", B, k.device)
+    if k.shape[2] == 0:
+        return
+    with torch.cuda.device(k.device):
+        fa_kv4_write(k.data_ptr(), v.data_ptr(), *(t.data_ptr() for t in cache), sp, cp, B, Hkv,
+                     k.shape[2], cap, d, _stream_handle(k))
+
+
+def kv4_read(cache, n: int, start=None, k=None, v=None):
+    """K, V [B, Hkv, n, d] bf16: what positions start[b] .. start[b]+n-1 of the cache stand for
+    (int32 [B] on the GPU, or None: 0)."""
+    import torch
+    B, Hkv, cap, d = _kv4(cache)
+    n = int(n)
+    if n < 0:
+        raise ValueError("n must not be negative")
+    k = _out(k, "k", (B, Hkv, n, d), torch.bfloat16, cache.k_codes)
+    v = _out(v, "v", (B, Hkv, n, d), torch.bfloat16, cache.k_codes)
+    sp = _int32_vector(start, "start", B, cache.k_codes.device)
+    if n > 0:
+        with torch.cuda.device(k.device):
+            fa_kv4_read(*(t.data_ptr() for t in cache), k.data_ptr(), v.data_ptr(), sp, B, Hkv, n, cap,
+                        d, _stream_handle(k))
+    return k, v
+
+
+def decode_kv4(q, cache, seqlens_k=None, causal: bool = False, scale: float | None = None,
+               softcap: float = 0.0, alibi_slopes=None, num_splits: int | None = None, out=None,
+               lse=None, workspace=None):
+    """Attention of q [B, Hq, Nq, d] bf16 against a 4-bit cache (KV4Cache), of which the first
+    seqlens_k[b] tokens are valid (int32 [B] on the GPU, or None: all).  Causal: the Nq queries
+    are the last Nq positions.  softcap c > 0: scores c tanh(x / c); alibi_slopes fp32 [Hq]:
+    slope |i - j| taken off.  Returns (O, LSE); rows that see no key get O = 0, LSE = -inf."""
+    import torch
+    B, Hkv, cap, d = _kv4(cache)
+    _need(q, "q")
+    if q.dim() != 4 or q.shape[0] != B or q.shape[3] != d:
+        raise ValueError(f"expected q [{B}, Hq, Nq, {d}], got {tuple(q.shape)}")
+    _, Hq, Nq, _ = q.shape
+    _same_device(q, cache.k_codes, workspace)
+    lens_ptr = _int32_vector(seqlens_k, "seqlens_k", B, q.device)
+    slopes_ptr = _slopes(alibi_slopes, Hq, q.device)
+    scale = default_scale(d) if scale is None else scale
+    with torch.cuda.device(q.device):
+        if num_splits is None:
+            num_splits = fa_decode_kv4_num_splits(B, Hq, Hkv, Nq, cap, d)
+            if num_splits < 1:
+                raise FAError(FA_ERR_GQA if Hq % Hkv else FA_ERR_UNSUPPORTED, "fa_decode_kv4_num_splits")
+        nbytes = fa_decode_kv4_workspace_bytes(B, Hq, Hkv, Nq, cap, d, num_splits)
+        if workspace is None and nbytes > 0:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        o = _out(out, "out", q.shape, torch.bfloat16, q)
+        l = _out(lse, "lse", (B, Hq, Nq), torch.float32, q)
+        ws_ptr = None if workspace is None else workspace.data_ptr()
+        ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+        fa_decode_kv4(q.data_ptr(), *(t.data_ptr() for t in cache), o.data_ptr(), l.data_ptr(), lens_ptr,
+                      slopes_ptr, ws_ptr, ws_bytes, B, Hq, Hkv, Nq, cap, d, causal, num_splits, softcap,
+                      scale, _stream_handle(q))
     return o, l
 
 

@@ -311,6 +311,62 @@ int fa_decode_num_splits(int B, int Hq, int Hkv, int Nq, int Nk, int d);
 size_t fa_decode_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d, int num_splits);
 
 /*
+ * A key/value cache held in 4 bits, written token by token, read back, and attended to.
+ * The pages name memory as the limit of long contexts and give no quantised cache; the
+ * format is this library's own.  For B batch entries, Hkv heads and `cap` tokens (a multiple
+ * of 64, B * Hkv * cap < 2^31) the cache is four arrays, all 16-byte aligned:
+ *   k_codes, v_codes   uint8 [B, Hkv, cap, d / 2]
+ *   k_params, v_params fp16  [B, Hkv, cap, 2 * d / 32]
+ * Channel c of a token stands for m + n s, with its code n in 0..15 and the step s and
+ * minimum m (fp16) of its group of 32 channels:
+ *   m = the largest fp16 number not above the group's least value,
+ *   s = the smallest one with m + 15 s not below its largest value,
+ *   n = the code nearest to the value, the upper one at a tie (0 where s = 0),
+ * after the values have been clamped to +-57344.  A group with a NaN or an infinity has
+ * m = NaN and reads back as NaN.  The stored bits are a pure function of the values.
+ *   codes: 32-bit little-endian words of 8 channels, the first one in the lowest 4 bits; V's
+ *          words follow the channels, K's word of channels 32 i + 8 c .. + 7 is word
+ *          c * (d / 32) + i.
+ *   params: V: s_0, m_0, s_1, m_1, ...;  K: s_0 .. s_(d/32-1), m_0 .. m_(d/32-1).
+ *
+ * fa_kv4_write quantises n new tokens per batch entry, k and v [B, Hkv, n, d] bf16, into
+ * positions start[b] .. start[b] + n - 1.  start: DEVICE int32 [B], or NULL for 0; counts:
+ * DEVICE int32 [B], only the first counts[b] tokens of entry b are written (NULL: n).  n = 0
+ * and counts[b] <= 0 write nothing.  Positions outside 0 .. cap - 1 are not written and are
+ * reported as FA_ERR_SEQLENS (fa_device_status); nothing else of the cache changes.
+ *
+ * fa_kv4_read writes the values of positions start[b] .. start[b] + n - 1, rounded to bf16,
+ * to k and v [B, Hkv, n, d].  Positions outside the cache leave their rows unwritten and are
+ * reported as FA_ERR_SEQLENS.
+ */
+int fa_kv4_write(const void *k, const void *v, void *k_codes, void *k_params, void *v_codes,
+                 void *v_params, const int *start, const int *counts, int B, int Hkv, int n,
+                 int cap, int d, void *stream);
+int fa_kv4_read(const void *k_codes, const void *k_params, const void *v_codes,
+                const void *v_params, void *k, void *v, const int *start, int B, int Hkv, int n,
+                int cap, int d, void *stream);
+
+/*
+ * Decode over the 4-bit cache: fa_decode with the cache of fa_kv4_write in place of k and v
+ * (seqlens_k clamped to [0, cap], NULL: cap), and with scores that may be changed:
+ *   softcap: 0, or c > 0: each scaled score x becomes c tanh(x / c);
+ *   alibi_slopes: NULL, or DEVICE fp32 [Hq]: slope[h] * |i - j| is then taken off, with
+ *        i = seqlens_k[b] - Nq + t the position of new row t and j that of the key.
+ * What lies behind the last valid token of the cache is not looked at (it may be
+ * uninitialised).  Rows that see no key get O = 0 and LSE = -inf.  Limits: (Hq / Hkv) * Nq
+ * <= 128, B * Hkv <= 65535, num_splits in 1 .. 1024; workspace and num_splits as for
+ * fa_decode, from the two functions below.
+ */
+int fa_decode_kv4(const void *q, const void *k_codes, const void *k_params, const void *v_codes,
+                  const void *v_params, void *o, float *lse, const int *seqlens_k,
+                  const float *alibi_slopes, void *workspace, size_t workspace_bytes, int B,
+                  int Hq, int Hkv, int Nq, int cap, int d, int causal, int num_splits,
+                  float softcap, float scale, void *stream);
+int fa_decode_kv4_num_splits(int B, int Hq, int Hkv, int Nq, int cap, int d);
+size_t fa_decode_kv4_workspace_bytes(int B, int Hq, int Hkv, int Nq, int cap, int d,
+                                     int num_splits);
+
+/*
  * Merge of `num_parts` partial attention results over disjoint key sets (the reduction
  * that fa_decode uses, exposed for callers that compute the parts themselves, e.g. over
  * key ranges held by different devices):
