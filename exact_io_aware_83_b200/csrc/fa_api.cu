@@ -182,6 +182,25 @@ bool device_ready() {
     ok = ok && set_smem(fa::fa_decode_kernel<256, 16>, fa::DecodeLayout<256, 16>::kSmemBytes);
     ok = ok && set_smem(fa::fa_decode_kernel<256, 32>, fa::DecodeLayout<256, 32>::kSmemBytes);
     ok = ok && set_smem(fa::fa_decode_kernel<256, 64>, fa::DecodeLayout<256, 64>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_fwd_kernel<64, fa::kAttnScore>, fa::FwdLayout<64>::kSmemBytesScore);
+    ok = ok && set_smem(fa::fa_fwd_kernel<128, fa::kAttnScore>, fa::FwdLayout<128>::kSmemBytesScore);
+    ok = ok && regs_at_least(fa::fa_fwd_kernel<64, fa::kAttnScore>, fa::kFwdRegsLaunch);
+    ok = ok && regs_at_least(fa::fa_fwd_kernel<128, fa::kAttnScore>, fa::kFwdRegsLaunch);
+    ok = ok && set_smem(fa::fa_fwd_d256_kernel<fa::kAttnScore>, fa::FwdD256Layout::kSmemBytesScore);
+    ok = ok && set_smem(fa_bwd_main_kernel<64, 64, 64, fa::kAttnScore>, BwdLayout<64, 64, 64>::kSmemBytesScore);
+    ok = ok && set_smem(fa_bwd_main_kernel<128, 128, 64, fa::kAttnScore>, BwdLayout<128, 128, 64>::kSmemBytesScore);
+    ok = ok && set_smem(fa_bwd_main_kernel<256, 128, 32, fa::kAttnScore>, BwdLayout<256, 128, 32>::kSmemBytesScore);
+    ok = ok && set_smem(fa::fa_decode_kernel<64, 16, true>, fa::DecodeLayout<64, 16>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kernel<64, 32, true>, fa::DecodeLayout<64, 32>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kernel<64, 64, true>, fa::DecodeLayout<64, 64>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kernel<64, 128, true>, fa::DecodeLayout<64, 128>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kernel<128, 16, true>, fa::DecodeLayout<128, 16>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kernel<128, 32, true>, fa::DecodeLayout<128, 32>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kernel<128, 64, true>, fa::DecodeLayout<128, 64>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kernel<128, 128, true>, fa::DecodeLayout<128, 128>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kernel<256, 16, true>, fa::DecodeLayout<256, 16>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kernel<256, 32, true>, fa::DecodeLayout<256, 32>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kernel<256, 64, true>, fa::DecodeLayout<256, 64>::kSmemBytes);
     using fa::FwdPLayout;
     ok = ok && set_smem(fa::fa_fwd_persist_kernel<64, fa::kAttnFull>, FwdPLayout<64>::kSmemBytes);
     ok = ok && set_smem(fa::fa_fwd_persist_kernel<64, fa::kAttnCausal>, FwdPLayout<64>::kSmemBytes);
@@ -268,6 +287,26 @@ void timer_stop(int which, int slot, cudaStream_t s) {
   if (cudaEventRecord(g_timer.ev[which][slot][1], s) == cudaSuccess) g_timer.count[which] = slot + 1;
 }
 
+// The two arguments that change the scores: a cap (0: none) and a slope per query head
+// (nullptr: none).
+int check_score_args(float softcap, const float *slopes) {
+  if (!(softcap >= 0.f) || !std::isfinite(softcap)) return FA_ERR_INVALID_ARG;
+  if (reinterpret_cast<uintptr_t>(slopes) & 3u) return FA_ERR_ALIGN;
+  return FA_OK;
+}
+
+fa::ScoreCfg make_score(float softcap, const float *slopes, const int *key_range, int causal, float scale) {
+  fa::ScoreCfg c{};
+  if (softcap > 0.f) {
+    c.cap_in = static_cast<float>(static_cast<double>(scale) / softcap);
+    c.cap_log2 = static_cast<float>(softcap * 1.4426950408889634);
+  }
+  c.slopes = slopes;
+  c.range = reinterpret_cast<const int2 *>(key_range);
+  c.causal = causal;
+  return c;
+}
+
 int check_sizes(int B, int Hq, int Hkv, int N, int d, float scale) {
   if (B < 1 || Hq < 1 || Hkv < 1 || N < 1) return FA_ERR_INVALID_ARG;
   if (!(scale > 0.f) || !std::isfinite(scale)) return FA_ERR_INVALID_ARG;
@@ -352,17 +391,19 @@ size_t decode_workspace(int B, int Hq, int Nq, int d, int splits) {
 
 template <int D, int RP>
 void launch_decode(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
-                   const fa::DecodeParams &p, unsigned grid, cudaStream_t s) {
-  fa::fa_decode_kernel<D, RP><<<grid, fa::kDecodeThreads, fa::DecodeLayout<D, RP>::kSmemBytes, s>>>(tq, tk, tv, p);
+                   const fa::DecodeParams &p, unsigned grid, bool score, cudaStream_t s) {
+  constexpr int smem = fa::DecodeLayout<D, RP>::kSmemBytes;
+  if (score) fa::fa_decode_kernel<D, RP, true><<<grid, fa::kDecodeThreads, smem, s>>>(tq, tk, tv, p);
+  else fa::fa_decode_kernel<D, RP><<<grid, fa::kDecodeThreads, smem, s>>>(tq, tk, tv, p);
 }
 
 template <int D>
 void launch_decode_d(int RP, const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
-                     const fa::DecodeParams &p, unsigned grid, cudaStream_t s) {
-  if (RP == 16) launch_decode<D, 16>(tq, tk, tv, p, grid, s);
-  else if (RP == 32) launch_decode<D, 32>(tq, tk, tv, p, grid, s);
-  else if (RP == 64) launch_decode<D, 64>(tq, tk, tv, p, grid, s);
-  else if constexpr (D != 256) launch_decode<D, 128>(tq, tk, tv, p, grid, s);
+                     const fa::DecodeParams &p, unsigned grid, bool score, cudaStream_t s) {
+  if (RP == 16) launch_decode<D, 16>(tq, tk, tv, p, grid, score, s);
+  else if (RP == 32) launch_decode<D, 32>(tq, tk, tv, p, grid, score, s);
+  else if (RP == 64) launch_decode<D, 64>(tq, tk, tv, p, grid, score, s);
+  else if constexpr (D != 256) launch_decode<D, 128>(tq, tk, tv, p, grid, score, s);
 }
 
 void launch_merge(const float *o_part, const float *lse_part, void *o, float *lse, int S, long long rows,
@@ -394,14 +435,6 @@ int check_kv4_decode(int B, int Hq, int Hkv, int Nq, int cap, int d, float scale
   if (static_cast<long long>(Hq / Hkv) * Nq > 128 || static_cast<long long>(B) * Hkv > 65535 ||
       static_cast<long long>(B) * Hq * Nq >= (1ll << 31))
     return FA_ERR_UNSUPPORTED;
-  return FA_OK;
-}
-
-// The two arguments that change the scores: a cap (0: none) and a slope per query head
-// (nullptr: none).
-int check_score_args(float softcap, const float *slopes) {
-  if (!(softcap >= 0.f) || !std::isfinite(softcap)) return FA_ERR_INVALID_ARG;
-  if (reinterpret_cast<uintptr_t>(slopes) & 3u) return FA_ERR_ALIGN;
   return FA_OK;
 }
 
@@ -437,15 +470,16 @@ void launch_kv4(const fa::KV4DecodeParams &p, cudaStream_t s) {
 template <int D, int MODE, bool DROP>
 void launch_fwd_d(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const CUtensorMap &to,
                   const FwdParams &p, unsigned units, cudaStream_t s) {
-  constexpr bool sparse = MODE == fa::kAttnSparse;
-  if constexpr (D == 256)
-    fa::fa_fwd_d256_kernel<MODE, DROP><<<units, fa::kFwdD256Threads,
-                                         sparse ? fa::FwdD256Layout::kSmemBytesSparse : fa::FwdD256Layout::kSmemBytes,
-                                         s>>>(tq, tk, tv, to, p);
-  else
-    fa::fa_fwd_kernel<D, MODE, DROP><<<units, fa::kFwdThreads,
-                                       sparse ? fa::FwdLayout<D>::kSmemBytesSparse : fa::FwdLayout<D>::kSmemBytes,
-                                       s>>>(tq, tk, tv, to, p);
+  constexpr bool sparse = MODE == fa::kAttnSparse, score = MODE == fa::kAttnScore;
+  if constexpr (D == 256) {
+    using L = fa::FwdD256Layout;
+    constexpr int smem = sparse ? L::kSmemBytesSparse : score ? L::kSmemBytesScore : L::kSmemBytes;
+    fa::fa_fwd_d256_kernel<MODE, DROP><<<units, fa::kFwdD256Threads, smem, s>>>(tq, tk, tv, to, p);
+  } else {
+    using L = fa::FwdLayout<D>;
+    constexpr int smem = sparse ? L::kSmemBytesSparse : score ? L::kSmemBytesScore : L::kSmemBytes;
+    fa::fa_fwd_kernel<D, MODE, DROP><<<units, fa::kFwdThreads, smem, s>>>(tq, tk, tv, to, p);
+  }
 }
 
 // Forward scheduler for dense full and causal attention (d = 64, 128): the persistent
@@ -482,6 +516,7 @@ void launch_fwd_mode(const CUtensorMap &tq, const CUtensorMap &tk, const CUtenso
   else if (drop) launch_fwd_d<D, fa::kAttnFull, true>(tq, tk, tv, to, p, units, s);
   else if (mode == fa::kAttnGeneral) launch_fwd_d<D, fa::kAttnGeneral, false>(tq, tk, tv, to, p, units, s);
   else if (mode == fa::kAttnSparse) launch_fwd_d<D, fa::kAttnSparse, false>(tq, tk, tv, to, p, units, s);
+  else if (mode == fa::kAttnScore) launch_fwd_d<D, fa::kAttnScore, false>(tq, tk, tv, to, p, units, s);
   else if (mode == fa::kAttnCausal) launch_fwd_d<D, fa::kAttnCausal, false>(tq, tk, tv, to, p, units, s);
   else launch_fwd_d<D, fa::kAttnFull, false>(tq, tk, tv, to, p, units, s);
 }
@@ -506,6 +541,7 @@ int launch_fwd(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &
   // (causal d = 256 was not measured).
   auto order = [&](int levels) {
     if (mode == fa::kAttnCausal) return p.nqb <= 16 ? 1 : levels;
+    if (mode == fa::kAttnScore) return 1;
     if (mode == fa::kAttnSparse || (mode == fa::kAttnGeneral && p.cu_q == nullptr)) return 1;
     return levels;
   };
@@ -599,6 +635,75 @@ int check_blocksparse(const unsigned char *mask, int Hq, int Hkv, int N, int d, 
                              : fa::BwdLayout<256, 128, 32>::kSparseBitmapBytes;
   if (words * 4 > cap) return FA_ERR_UNSUPPORTED;
   return FA_OK;
+}
+
+// Changed scores: the backward keeps one bit per 128-row query block in shared memory, and the
+// spans of the query blocks are found by a grid with the batch in y.
+int check_score_bwd(int B, int N, int d) {
+  const long long words = ((N + 127) / 128 + 31) / 32;
+  const int cap = d == 64 ? fa::BwdLayout<64, 64, 64>::kScoreBitmapBytes
+                  : d == 128 ? fa::BwdLayout<128, 128, 64>::kScoreBitmapBytes
+                             : fa::BwdLayout<256, 128, 32>::kScoreBitmapBytes;
+  return words * 4 > cap || B > 65535 ? FA_ERR_UNSUPPORTED : FA_OK;
+}
+
+// fa_decode, or with `score` its form with changed scores.
+int run_decode(const void *q, const void *k, const void *v, void *o, float *lse, const int *seqlens_k,
+               void *workspace, size_t workspace_bytes, int B, int Hq, int Hkv, int Nq, int Nk, int d,
+               int causal, int num_splits, float scale, void *stream, const fa::ScoreCfg *score) {
+  if (!q || !k || !v || !o || !lse) return FA_ERR_INVALID_ARG;
+  if (causal != 0 && causal != 1) return FA_ERR_INVALID_ARG;
+  if (num_splits < 1 || num_splits > kMaxDecodeSplits) return FA_ERR_INVALID_ARG;
+  int rc = check_decode_sizes(B, Hq, Hkv, Nq, Nk, d, scale);
+  if (rc != FA_OK) return rc;
+  if (static_cast<long long>(B) * Hkv * num_splits >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
+  const size_t need = decode_workspace(B, Hq, Nq, d, num_splits);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return FA_ERR_WORKSPACE;
+  const void *ptrs[] = {q, k, v, o, lse};
+  for (const void *ptr : ptrs)
+    if (!aligned16(ptr)) return FA_ERR_ALIGN;
+  if ((need > 0 && !aligned16(workspace)) || (reinterpret_cast<uintptr_t>(seqlens_k) & 3u)) return FA_ERR_ALIGN;
+  if (!device_ready()) return FA_ERR_CUDA;
+
+  const int g = Hq / Hkv, R = g * Nq, RP = decode_rows_padded(R);
+  CUtensorMap tq, tk, tv;
+  // Q viewed as [B * Hkv][R][d]: the rows of the query heads that share a K/V head.
+  if (!make_map_bf16(&tq, q, d, R, static_cast<long long>(B) * Hkv, RP) ||
+      !make_map_bf16(&tk, k, d, Nk, static_cast<long long>(B) * Hkv, 128) ||
+      !make_map_bf16(&tv, v, d, Nk, static_cast<long long>(B) * Hkv, 128)) {
+    if (debug_enabled()) std::fprintf(stderr, "[fa] cuTensorMapEncodeTiled failed (fa_decode)\n");
+    return FA_ERR_CUDA;
+  }
+  const size_t rows = static_cast<size_t>(B) * Hq * Nq;
+  fa::DecodeParams p;
+  p.lens = seqlens_k;
+  p.o = static_cast<__nv_bfloat16 *>(o);
+  p.lse = lse;
+  p.o_part = num_splits > 1 ? static_cast<float *>(workspace) : nullptr;
+  p.lse_part = num_splits > 1
+                   ? reinterpret_cast<float *>(static_cast<char *>(workspace) +
+                                               fa::pad256(static_cast<size_t>(num_splits) * rows * d * 4))
+                   : nullptr;
+  p.B = B;
+  p.Hkv = Hkv;
+  p.Nq = Nq;
+  p.Nk = Nk;
+  p.R = R;
+  p.splits = num_splits;
+  const int per = (Nk + num_splits - 1) / num_splits;
+  p.chunk = (per + 127) / 128 * 128;
+  p.causal = causal;
+  p.sl2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  p.score = score ? *score : fa::ScoreCfg{};
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const unsigned grid = static_cast<unsigned>(B) * Hkv * num_splits;
+  const int tslot = timer_start(2, s);
+  if (d == 64) launch_decode_d<64>(RP, tq, tk, tv, p, grid, score != nullptr, s);
+  else if (d == 128) launch_decode_d<128>(RP, tq, tk, tv, p, grid, score != nullptr, s);
+  else launch_decode_d<256>(RP, tq, tk, tv, p, grid, score != nullptr, s);
+  timer_stop(2, tslot, s);
+  if (num_splits > 1) launch_merge(p.o_part, p.lse_part, o, lse, num_splits, static_cast<long long>(rows), d, s);
+  return cuda_ok(cudaGetLastError(), "fa_decode launch") ? FA_OK : FA_ERR_CUDA;
 }
 
 }  // namespace
@@ -902,6 +1007,68 @@ int fa_bwd_blocksparse(const void *q, const void *k, const void *v, const void *
                         block_mask);
 }
 
+int fa_fwd_score(const void *q, const void *k, const void *v, void *o, float *lse, const float *alibi_slopes,
+                 const int *key_range, int B, int Hq, int Hkv, int N, int d, int causal, float softcap, float scale,
+                 void *stream) {
+  if (!q || !k || !v || !o || !lse) return FA_ERR_INVALID_ARG;
+  if (causal != 0 && causal != 1) return FA_ERR_INVALID_ARG;
+  int rc = check_sizes(B, Hq, Hkv, N, d, scale);
+  if (rc == FA_OK) rc = check_score_args(softcap, alibi_slopes);
+  if (rc != FA_OK) return rc;
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || !aligned16(o) || !aligned16(lse) ||
+      (reinterpret_cast<uintptr_t>(key_range) & 7u))
+    return FA_ERR_ALIGN;
+  if (!device_ready()) return FA_ERR_CUDA;
+  const int kv_rows = d == 256 ? 64 : 128;
+  CUtensorMap tq, tk, tv, to;
+  if (!make_map_bf16(&tq, q, d, N, static_cast<long long>(B) * Hq, 128) ||
+      !make_map_bf16(&tk, k, d, N, static_cast<long long>(B) * Hkv, kv_rows) ||
+      !make_map_bf16(&tv, v, d, N, static_cast<long long>(B) * Hkv, kv_rows) ||
+      !make_map_bf16(&to, o, d, N, static_cast<long long>(B) * Hq, 128))
+    return FA_ERR_CUDA;
+  FwdParams p;
+  p.lse = lse;
+  p.o = static_cast<__nv_bfloat16 *>(o);
+  p.cu_q = p.cu_k = nullptr;
+  p.B = B;
+  p.Hq = Hq;
+  p.Hkv = Hkv;
+  p.N = N;
+  p.total_q = p.total_k = 0;
+  p.nqb = (N + 127) / 128;
+  p.left = p.right = -1;
+  p.sl2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  p.score = make_score(softcap, alibi_slopes, key_range, causal, scale);
+  return launch_fwd(tq, tk, tv, to, p, d, fa::kAttnScore, static_cast<cudaStream_t>(stream));
+}
+
+size_t fa_bwd_score_workspace_bytes(int B, int Hq, int Hkv, int N, int d) {
+  if (check_sizes(B, Hq, Hkv, N, d, 1.0f) != FA_OK) return 0;
+  return fa::bwd_workspace_bytes(B, Hq, N, d) + fa::pad256(static_cast<size_t>(B) * ((N + 127) / 128) * 8);
+}
+
+int fa_bwd_score(const void *q, const void *k, const void *v, const void *o, const float *lse, const void *dout,
+                 void *dq, void *dk, void *dv, void *workspace, size_t workspace_bytes, const float *alibi_slopes,
+                 const int *key_range, int B, int Hq, int Hkv, int N, int d, int causal, float softcap, float scale,
+                 void *stream) {
+  if (!q || !k || !v || !o || !lse || !dout || !dq || !dk || !dv) return FA_ERR_INVALID_ARG;
+  if (causal != 0 && causal != 1) return FA_ERR_INVALID_ARG;
+  int rc = check_sizes(B, Hq, Hkv, N, d, scale);
+  if (rc == FA_OK) rc = check_score_args(softcap, alibi_slopes);
+  if (rc == FA_OK) rc = check_score_bwd(B, N, d);
+  if (rc != FA_OK) return rc;
+  if (!workspace || workspace_bytes < fa_bwd_score_workspace_bytes(B, Hq, Hkv, N, d)) return FA_ERR_WORKSPACE;
+  const void *ptrs[] = {q, k, v, o, lse, dout, dq, dk, dv, workspace};
+  for (const void *ptr : ptrs)
+    if (!aligned16(ptr)) return FA_ERR_ALIGN;
+  if (reinterpret_cast<uintptr_t>(key_range) & 7u) return FA_ERR_ALIGN;
+  if (!device_ready()) return FA_ERR_CUDA;
+  const fa::ScoreCfg score = make_score(softcap, alibi_slopes, key_range, causal, scale);
+  return fa::bwd_launch(q, k, v, o, lse, dout, dq, dk, dv, workspace, B, Hq, Hkv, N, d, -1, causal ? 0 : -1, scale,
+                        static_cast<cudaStream_t>(stream), encode_fn(), &timer_start, &timer_stop, nullptr, nullptr,
+                        nullptr, bwd_order(B, Hkv, N, key_range ? N : -1, causal ? 0 : -1), &score);
+}
+
 int fa_set_fwd_scheduler(int persistent) {
   if (persistent != 0 && persistent != 1) return FA_ERR_INVALID_ARG;
   return g_fwd_persistent.exchange(persistent);
@@ -989,58 +1156,18 @@ size_t fa_decode_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d, 
 int fa_decode(const void *q, const void *k, const void *v, void *o, float *lse, const int *seqlens_k,
               void *workspace, size_t workspace_bytes, int B, int Hq, int Hkv, int Nq, int Nk, int d,
               int causal, int num_splits, float scale, void *stream) {
-  if (!q || !k || !v || !o || !lse) return FA_ERR_INVALID_ARG;
-  if (causal != 0 && causal != 1) return FA_ERR_INVALID_ARG;
-  if (num_splits < 1 || num_splits > kMaxDecodeSplits) return FA_ERR_INVALID_ARG;
-  int rc = check_decode_sizes(B, Hq, Hkv, Nq, Nk, d, scale);
-  if (rc != FA_OK) return rc;
-  if (static_cast<long long>(B) * Hkv * num_splits >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
-  const size_t need = decode_workspace(B, Hq, Nq, d, num_splits);
-  if (need > 0 && (!workspace || workspace_bytes < need)) return FA_ERR_WORKSPACE;
-  const void *ptrs[] = {q, k, v, o, lse};
-  for (const void *ptr : ptrs)
-    if (!aligned16(ptr)) return FA_ERR_ALIGN;
-  if ((need > 0 && !aligned16(workspace)) || (reinterpret_cast<uintptr_t>(seqlens_k) & 3u)) return FA_ERR_ALIGN;
-  if (!device_ready()) return FA_ERR_CUDA;
+  return run_decode(q, k, v, o, lse, seqlens_k, workspace, workspace_bytes, B, Hq, Hkv, Nq, Nk, d, causal, num_splits,
+                    scale, stream, nullptr);
+}
 
-  const int g = Hq / Hkv, R = g * Nq, RP = decode_rows_padded(R);
-  CUtensorMap tq, tk, tv;
-  // Q viewed as [B * Hkv][R][d]: the rows of the query heads that share a K/V head.
-  if (!make_map_bf16(&tq, q, d, R, static_cast<long long>(B) * Hkv, RP) ||
-      !make_map_bf16(&tk, k, d, Nk, static_cast<long long>(B) * Hkv, 128) ||
-      !make_map_bf16(&tv, v, d, Nk, static_cast<long long>(B) * Hkv, 128)) {
-    if (debug_enabled()) std::fprintf(stderr, "[fa] cuTensorMapEncodeTiled failed (fa_decode)\n");
-    return FA_ERR_CUDA;
-  }
-  const size_t rows = static_cast<size_t>(B) * Hq * Nq;
-  fa::DecodeParams p;
-  p.lens = seqlens_k;
-  p.o = static_cast<__nv_bfloat16 *>(o);
-  p.lse = lse;
-  p.o_part = num_splits > 1 ? static_cast<float *>(workspace) : nullptr;
-  p.lse_part = num_splits > 1
-                   ? reinterpret_cast<float *>(static_cast<char *>(workspace) +
-                                               fa::pad256(static_cast<size_t>(num_splits) * rows * d * 4))
-                   : nullptr;
-  p.B = B;
-  p.Hkv = Hkv;
-  p.Nq = Nq;
-  p.Nk = Nk;
-  p.R = R;
-  p.splits = num_splits;
-  const int per = (Nk + num_splits - 1) / num_splits;
-  p.chunk = (per + 127) / 128 * 128;
-  p.causal = causal;
-  p.sl2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-  cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const unsigned grid = static_cast<unsigned>(B) * Hkv * num_splits;
-  const int tslot = timer_start(2, s);
-  if (d == 64) launch_decode_d<64>(RP, tq, tk, tv, p, grid, s);
-  else if (d == 128) launch_decode_d<128>(RP, tq, tk, tv, p, grid, s);
-  else launch_decode_d<256>(RP, tq, tk, tv, p, grid, s);
-  timer_stop(2, tslot, s);
-  if (num_splits > 1) launch_merge(p.o_part, p.lse_part, o, lse, num_splits, static_cast<long long>(rows), d, s);
-  return cuda_ok(cudaGetLastError(), "fa_decode launch") ? FA_OK : FA_ERR_CUDA;
+int fa_decode_score(const void *q, const void *k, const void *v, void *o, float *lse, const int *seqlens_k,
+                    const float *alibi_slopes, void *workspace, size_t workspace_bytes, int B, int Hq, int Hkv,
+                    int Nq, int Nk, int d, int causal, int num_splits, float softcap, float scale, void *stream) {
+  const int rc = check_score_args(softcap, alibi_slopes);
+  if (rc != FA_OK) return rc;
+  const fa::ScoreCfg score = make_score(softcap, alibi_slopes, nullptr, causal, scale);
+  return run_decode(q, k, v, o, lse, seqlens_k, workspace, workspace_bytes, B, Hq, Hkv, Nq, Nk, d, causal, num_splits,
+                    scale, stream, &score);
 }
 
 int fa_kv4_write(const void *k, const void *v, void *k_codes, void *k_params, void *v_codes, void *v_params,

@@ -11,7 +11,9 @@
 //   dV_j   = sum_i P_ij do_i,  dK_j = scale sum_i dS_ij q_i,  dQ_i = scale sum_j dS_ij k_j
 // (dK, dV summed over the query heads that share a K/V head), with P_ij = 0 for keys
 // outside query i's window i - left <= j <= i + right (causal: left unlimited, right 0)
-// or, block-sparse, outside the enabled 128 x 128 blocks of the query head's mask.
+// or, block-sparse, outside the enabled 128 x 128 blocks of the query head's mask.  With
+// changed scores s_ij (fa_score.cuh) P_ij = exp(s_ij - LSE_i) and dS_ij takes the factor
+// 1 - tanh^2(x_ij / cap) of a cap.
 //
 // Three kernels on one stream:
 //  1. fa_bwd_pre:  Delta_i = <dO_i, O_i> (fp32) and a zeroed fp32 dQ accumulator.
@@ -36,6 +38,7 @@
 #pragma once
 
 #include "fa_common.cuh"
+#include "fa_score.cuh"
 
 namespace fa {
 
@@ -111,6 +114,8 @@ struct BwdParams {
   const uint8_t *bmask;   // block-sparse: [B, Hq, nkb, nkb] 0/1 over 128 x 128 blocks
   int tsz;                // unit order: key-block levels per tier (see unit_order)
   int tail;               // unit order: heads taken level by level at the end
+  ScoreCfg score;         // changed scores (kAttnScore only)
+  const int2 *blocks;     // changed scores with key ranges: [B, nkb] span of each 128-row query block
 };
 
 // D: head dimension (contraction of S^T and dP^T); DH: output columns owned by a CTA
@@ -161,6 +166,15 @@ struct BwdLayout {
   static constexpr int kSparseBitmapBytes =
       (232448 - (kOffList + 16 + 1024)) / 4 * 4 < 8192 ? (232448 - (kOffList + 16 + 1024)) / 4 * 4 : 8192;
   static constexpr int kSmemBytesSparse = kOffList + 16 + kSparseBitmapBytes + 1024;
+  // Changed scores only: after the header, per stage the first visible key and the end of the
+  // visible keys of each query row, and a flag (every row sees the whole key block); then
+  // one bitmap of query blocks, the same for every head of the group.
+  static constexpr int kOffRange = kOffList + 16;                  // [stage][lo | hi][BQ] int
+  static constexpr int kOffScoreFlag = kOffRange + kQStages * 2 * BQ * 4;  // [stage], padded to 16 bytes
+  static constexpr int kOffScoreBits = kOffScoreFlag + 16;
+  static constexpr int kScoreBitmapBytes =
+      (232448 - (kOffScoreBits + 1024)) / 4 * 4 < 8192 ? (232448 - (kOffScoreBits + 1024)) / 4 * 4 : 8192;
+  static constexpr int kSmemBytesScore = kOffScoreBits + kScoreBitmapBytes + 1024;
   // tensor memory: dV | dK | S^T | dP^T | dQ^T
   static constexpr uint32_t kTmDV = 0;
   static constexpr uint32_t kTmDK = DH;
@@ -179,6 +193,7 @@ struct BwdLayout {
   }
   static_assert(kTmDQ + BQ <= 512, "tensor-memory budget");
   static_assert(kSmemBytesSparse <= 232448 && kSparseBitmapBytes >= 256, "shared-memory budget");
+  static_assert(kSmemBytesScore <= 232448 && kScoreBitmapBytes >= 256 && kOffRange % 16 == 0, "shared-memory budget");
   static_assert(BQ == 32 || BQ == 64, "query block");
 };
 
@@ -191,11 +206,13 @@ constexpr int kBwdThreads = 448;
 // block of the sequence has only those that start before N).  Each role walks the same
 // sequence with its own cursor.
 struct SparseSteps {
-  const uint32_t *bits;  // [g][W] words
-  int W, g, nqb, nsub, nsub_last;
+  const uint32_t *bits;  // [g][W] words (changed scores: [W], the same for every head)
+  int W, g, nqb, nsub, nsub_last, stride;
   int hh, qb, sub;
-  __device__ __forceinline__ void init(const uint32_t *bits_, int W_, int g_, int nqb_, int nsub_, int nsub_last_) {
+  __device__ __forceinline__ void init(const uint32_t *bits_, int W_, int g_, int nqb_, int nsub_, int nsub_last_,
+                                       int stride_) {
     bits = bits_;
+    stride = stride_;
     W = W_;
     g = g_;
     nqb = nqb_;
@@ -208,7 +225,7 @@ struct SparseSteps {
   // First set bit >= from in head hh's bitmap, or -1.
   __device__ __forceinline__ int find(int from) const {
     for (int w = from >> 5; w < W; ++w) {
-      uint32_t u = bits[hh * W + w];
+      uint32_t u = bits[hh * stride + w];
       if (w == (from >> 5)) u &= ~0u << (from & 31);
       if (u) return w * 32 + __ffs(u) - 1;
     }
@@ -284,13 +301,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     q_first = MODE == kAttnCausal ? kv0 / BQ : 0;
     nq = (p.N + BQ - 1) / BQ - q_first;
   }
+  constexpr bool SCORE = MODE == kAttnScore;
+  constexpr bool LISTED = MODE == kAttnSparse || SCORE;  // steps from a bitmap of query blocks
   constexpr bool SPARSE = MODE == kAttnSparse;
-  constexpr bool GENLIKE = GEN || SPARSE;  // a key block may see no query at all
+  constexpr bool GENLIKE = GEN || LISTED;  // a key block may see no query at all
   int T = g * nq;  // steps: (query head of the group, query block); block-sparse: counted below
   const int spW = (p.nkb + 31) / 32;
   constexpr int kSub = 128 / BQ;
   const int spSubLast = (p.N - (p.nkb - 1) * 128 + BQ - 1) / BQ;
-  uint32_t *spbits = reinterpret_cast<uint32_t *>(smem + L::kOffList + 16);
+  uint32_t *spbits = reinterpret_cast<uint32_t *>(smem + (SCORE ? L::kOffScoreBits : L::kOffList + 16));
+  int *sc_range = reinterpret_cast<int *>(smem + L::kOffRange);
+  volatile int *sc_flag = reinterpret_cast<volatile int *>(smem + L::kOffScoreFlag);
   const int dcol0 = half * DH;  // first output column owned by this CTA
   // TMA coordinates (dimensions 1 and 2): dense maps are [B*H][N][cols], packed [total][H][cols].
   auto q_coords = [&](int hh, int row, int &c1, int &c2) {
@@ -352,11 +373,32 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (lane == 0) reinterpret_cast<int *>(smem + L::kOffList)[wq] = steps;
     }
   }
+  if constexpr (SCORE) {
+    // Query block qb sees this key block when the span of its rows meets it.
+    if (warp >= 8 && warp < 12) {
+      int steps = 0;
+      for (int w = warp - 8; w < spW; w += 4) {
+        const int qb = w * 32 + lane;
+        bool v = qb < p.nkb && (!p.score.causal || qb >= kb);
+        if (v && p.blocks) {
+          const int2 r = p.blocks[static_cast<size_t>(b) * p.nkb + qb];
+          v = r.x < kv0 + 128 && r.y > kv0;
+        }
+        const uint32_t u = __ballot_sync(0xffffffffu, v);
+        if (lane == 0) {
+          spbits[w] = u;
+          steps += __popc(u) * kSub;
+          if (w == spW - 1 && ((u >> ((p.nkb - 1) & 31)) & 1u)) steps -= kSub - spSubLast;
+        }
+      }
+      if (lane == 0) reinterpret_cast<int *>(smem + L::kOffList)[warp - 8] = steps * g;
+    }
+  }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = misc[0];
-  if constexpr (SPARSE) {
+  if constexpr (LISTED) {
     const int *hdr = reinterpret_cast<const int *>(smem + L::kOffList);
     T = hdr[0] + hdr[1] + hdr[2] + hdr[3];
   }
@@ -365,7 +407,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   auto step_q0 = [&](int i) { return (q_first + i % nq) * BQ; };
   // Block-sparse: each role's cursor, moved once per step before (h, q0) are used.
   SparseSteps cur;
-  if constexpr (SPARSE) cur.init(spbits, spW, g, p.nkb, kSub, spSubLast);
+  if constexpr (LISTED) cur.init(spbits, spW, g, p.nkb, kSub, spSubLast, SCORE ? 0 : spW);
 
   if (warp == 13) {
     // ================================================================ loader
@@ -388,8 +430,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       ok = warp_wait_bounded(bar(L::kBarQEmpty + st), (use & 1) ^ 1, abort_flag,
                              wait_site(3, L::kBarQEmpty + st, i));
       if (!ok) break;
-      if constexpr (SPARSE) cur.next();
-      const int h = SPARSE ? kvh * g + cur.hh : step_head(i), q0 = SPARSE ? cur.q0<BQ>() : step_q0(i);
+      if constexpr (LISTED) cur.next();
+      const int h = LISTED ? kvh * g + cur.hh : step_head(i), q0 = LISTED ? cur.q0<BQ>() : step_q0(i);
       if (lane == 0) {
         int c1, c2;
         q_coords(h, q0, c1, c2);
@@ -402,6 +444,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
       float *lse2 = vec + (st * 2) * BQ;
       float *dl = vec + (st * 2 + 1) * BQ;
+      bool whole = true;  // changed scores: every row of the step sees the whole key block
       for (int c = lane; c < BQ; c += 32) {
         const int q = q0 + c;
         // Query rows past the sequence get LSE = +inf, so their probabilities are exactly 0
@@ -410,6 +453,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         const bool live = q < sg.Lq;
         lse2[c] = live ? p.lse[vec_row(h, q)] * 1.4426950408889634f : INFINITY;
         dl[c] = live ? p.delta[vec_row(h, q)] : 0.f;
+        if constexpr (SCORE) {
+          // A row that sees no key has LSE = -inf and may share a block with rows that do.
+          if (lse2[c] == -INFINITY) lse2[c] = INFINITY;
+          int lo, hi;
+          row_range(p.score, b, q, p.N, lo, hi);
+          sc_range[(st * 2) * BQ + c] = lo;
+          sc_range[(st * 2 + 1) * BQ + c] = hi;
+          whole = whole && (!live || (lo <= kv0 && hi >= min(kv0 + 128, p.N)));
+        }
+      }
+      if constexpr (SCORE) {
+        whole = __all_sync(0xffffffffu, whole);
+        if (lane == 0) sc_flag[st] = whole;
       }
       // The stores above are ordered before lane 0's arrival by the warp barrier; the
       // barrier phase completes only when that arrival and the TMA bytes are both in.
@@ -510,12 +566,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const uint32_t tS = tmem + L::kTmS + lane_off + c0;
     const uint32_t tDP = tmem + L::kTmDP + lane_off + c0;
     const bool row_live = kv < sg.Lk;
-    const float sl2 = p.sl2;
+    const float sl2 = SCORE ? 1.f : p.sl2;  // changed scores are in log2 units already
     bool ok = true;
     for (int i = 0; ok && i < T; ++i) {
       const int st = i % QS;
-      if constexpr (SPARSE) cur.next();
-      const int q0 = (SPARSE ? cur.q0<BQ>() : step_q0(i)) + c0;  // first query column of this warpgroup
+      if constexpr (LISTED) cur.next();
+      const int q0 = (LISTED ? cur.q0<BQ>() : step_q0(i)) + c0;  // first query column of this warpgroup
       if (!(ok = warp_wait_bounded(bar(L::kBarQFull + st), (i / QS) & 1, abort_flag,
                                    wait_site(3, L::kBarQFull + st, i))))
         break;
@@ -524,9 +580,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const float4 *lse4 = reinterpret_cast<const float4 *>(vec + (st * 2) * BQ + c0);
       const float4 *dl4 = reinterpret_cast<const float4 *>(vec + (st * 2 + 1) * BQ + c0);
       float pr[HC];
+      float cgrad[SCORE ? HC : 1];  // changed scores: 1 - tanh^2
       {
         uint32_t rr[HC];
         if constexpr (HC == 32) tmem_ld_x32(tS, rr); else tmem_ld_x16(tS, rr);
+        if constexpr (SCORE) {
+          const float slope2 = p.score.slopes ? p.score.slopes[kvh * g + cur.hh] * kLog2e : 0.f;
+          const int qa = q0 - c0, side = qa + BQ - 1 <= kv0 ? -1 : (qa >= kv0 + 127 ? 1 : 0);
+          score_log2<HC, true>(rr, cgrad, p.score, p.sl2, slope2, kv, q0, side);
+        }
 #pragma unroll
         for (int c4 = 0; c4 < HC / 4; ++c4) {
           const float4 l = lse4[c4];
@@ -541,6 +603,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (!row_live) {
 #pragma unroll
         for (int c = 0; c < HC; ++c) pr[c] = 0.f;
+      } else if constexpr (SCORE) {
+        if (!sc_flag[st]) {
+          const int4 *lo4 = reinterpret_cast<const int4 *>(sc_range + (st * 2) * BQ + c0);
+          const int4 *hi4 = reinterpret_cast<const int4 *>(sc_range + (st * 2 + 1) * BQ + c0);
+#pragma unroll
+          for (int c4 = 0; c4 < HC / 4; ++c4) {
+            const int4 lo = lo4[c4], hi = hi4[c4];
+            if (kv < lo.x || kv >= hi.x) pr[4 * c4 + 0] = 0.f;
+            if (kv < lo.y || kv >= hi.y) pr[4 * c4 + 1] = 0.f;
+            if (kv < lo.z || kv >= hi.z) pr[4 * c4 + 2] = 0.f;
+            if (kv < lo.w || kv >= hi.w) pr[4 * c4 + 3] = 0.f;
+          }
+        }
       } else if (GEN && (p.left >= 0 || p.right >= 0)) {
         const int c_lo = p.right < 0 ? INT_MIN : kv - p.right - sg.dlt - q0;
         const int c_hi = p.left < 0 ? INT_MAX : kv + p.left - sg.dlt - q0;
@@ -592,6 +667,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::kBarP));
+      if constexpr (SCORE) {
+        if (p.score.cap_in > 0.f) {
+#pragma unroll
+          for (int c = 0; c < HC; ++c) pr[c] *= cgrad[c];  // dS = P (1 - tanh^2) (dP - Delta)
+        }
+      }
 
       if (!(ok = warp_wait_bounded(bar(L::kBarDP), i & 1, abort_flag, wait_site(3, L::kBarDP, i)))) break;
       tc_fence_after_sync();
@@ -708,8 +789,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::kBarDQEmpty));
-      if constexpr (SPARSE) cur.next();
-      const int h = SPARSE ? kvh * g + cur.hh : step_head(i), q0 = SPARSE ? cur.q0<BQ>() : step_q0(i);
+      if constexpr (LISTED) cur.next();
+      const int h = LISTED ? kvh * g + cur.hh : step_head(i), q0 = LISTED ? cur.q0<BQ>() : step_q0(i);
 #pragma unroll
       for (int hp = 0; hp < L::kDQHalves; ++hp) {
         // The previous reduce must have finished reading the staging buffer.
@@ -798,7 +879,8 @@ inline void bwd_launch_main(const CUtensorMap &tq, const CUtensorMap &tk, const 
                             const CUtensorMap &tdq, const BwdParams &p, unsigned grid, cudaStream_t s) {
   using L = BwdLayout<D, DH, BQ>;
   fa_bwd_main_kernel<D, DH, BQ, MODE, DROP>
-      <<<grid, kBwdThreads, MODE == kAttnSparse ? L::kSmemBytesSparse : L::kSmemBytes, s>>>(tq, tk, tv, tdo, tdk,
+      <<<grid, kBwdThreads,
+         MODE == kAttnSparse ? L::kSmemBytesSparse : MODE == kAttnScore ? L::kSmemBytesScore : L::kSmemBytes, s>>>(tq, tk, tv, tdo, tdk,
                                                                                            tdv, tdq, p);
 }
 
@@ -828,7 +910,7 @@ inline int bwd_launch_d(const void *q, const void *k, const void *v, const void 
                         const void *dout, void *dq, void *dk, void *dv, void *workspace, int B, int Hq,
                         int Hkv, int N, int left, int right, float scale, cudaStream_t s, EncodeTiledFnBwd enc,
                         TimerStartFn tstart, TimerStopFn tstop, const PackedSeqs *pk, const DropCfg *drop,
-                        const uint8_t *bmask, BwdOrder order) {
+                        const uint8_t *bmask, BwdOrder order, const ScoreCfg *score) {
   const long long rows = pk ? static_cast<long long>(pk->total_q) * Hq : static_cast<long long>(B) * Hq * N;
   float *delta = static_cast<float *>(workspace);
   float *dqacc = reinterpret_cast<float *>(static_cast<char *>(workspace) + pad256(static_cast<size_t>(rows) * 4));
@@ -875,6 +957,14 @@ inline int bwd_launch_d(const void *q, const void *k, const void *v, const void 
   p.sl2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   p.drop = drop ? *drop : DropCfg{};
   p.bmask = bmask;
+  p.score = score ? *score : ScoreCfg{};
+  p.blocks = nullptr;
+  if (score && score->range) {
+    // The spans of the query blocks, behind the dQ accumulator.
+    int2 *blocks = reinterpret_cast<int2 *>(static_cast<char *>(workspace) + bwd_workspace_bytes(B, Hq, N, D));
+    fa_score_blocks_kernel<<<dim3(static_cast<unsigned>(p.nkb), static_cast<unsigned>(B)), 128, 0, s>>>(*score, N, blocks);
+    p.blocks = blocks;
+  }
   // Unit order (unit_order): `order.tiers` tiers of key-block levels (1: head-major), the
   // last `order.tail` (b, kv head) rows level by level.
   const int tiers = order.tiers < 1 ? 1 : order.tiers;
@@ -887,7 +977,7 @@ inline int bwd_launch_d(const void *q, const void *k, const void *v, const void 
   // d = 256, and with 128-query steps at d = 128 from N = 4096 on.  Below that a CTA has
   // too few steps to repay the longer pipeline start of 128-query steps (measured on B200:
   // 128-query steps +4% at N = 8192, +2% at N = 4096, -5% at N = 2048).
-  const bool dense = !pk && !drop && !bmask && left < 0 && right <= 0;
+  const bool dense = !pk && !drop && !bmask && !score && left < 0 && right <= 0;
   if (dense && (D == 256 || (D == 128 && N >= kQ128MinN)) && grid > 0) {
     bool launched;
     if (D == 256)
@@ -903,7 +993,9 @@ inline int bwd_launch_d(const void *q, const void *k, const void *v, const void 
   } else if (grid > 0) {
     // Dense full and causal attention have their own variants; packed sequences and other
     // bands take the general one.
-    if (bmask)  // block-sparse: dense layout, causal or not (right = 0 or -1)
+    if (score)
+      bwd_launch_main<D, DH, BQ, kAttnScore>(tq, tk, tv, tdo, tdk, tdv, tdq, p, grid, s);
+    else if (bmask)  // block-sparse: dense layout, causal or not (right = 0 or -1)
       bwd_launch_main<D, DH, BQ, kAttnSparse>(tq, tk, tv, tdo, tdk, tdv, tdq, p, grid, s);
     else if (drop && right == 0)  // dropout: dense attention only (the host checks)
       bwd_launch_main<D, DH, BQ, kAttnCausal, true>(tq, tk, tv, tdo, tdk, tdv, tdq, p, grid, s);
@@ -929,16 +1021,17 @@ inline int bwd_launch(const void *q, const void *k, const void *v, const void *o
                       const void *dout, void *dq, void *dk, void *dv, void *workspace, int B, int Hq,
                       int Hkv, int N, int d, int left, int right, float scale, cudaStream_t s, Enc enc,
                       TimerStartFn tstart, TimerStopFn tstop, const PackedSeqs *pk = nullptr,
-                      const DropCfg *drop = nullptr, const uint8_t *bmask = nullptr, BwdOrder order = {1, 0}) {
+                      const DropCfg *drop = nullptr, const uint8_t *bmask = nullptr, BwdOrder order = {1, 0},
+                      const ScoreCfg *score = nullptr) {
   const EncodeTiledFnBwd e = reinterpret_cast<EncodeTiledFnBwd>(enc);
   if (d == 64)
     return bwd_launch_d<64, 64, 64>(q, k, v, o, lse, dout, dq, dk, dv, workspace, B, Hq, Hkv, N, left, right,
-                                    scale, s, e, tstart, tstop, pk, drop, bmask, order);
+                                    scale, s, e, tstart, tstop, pk, drop, bmask, order, score);
   if (d == 128)
     return bwd_launch_d<128, 128, 64>(q, k, v, o, lse, dout, dq, dk, dv, workspace, B, Hq, Hkv, N, left, right,
-                                      scale, s, e, tstart, tstop, pk, drop, bmask, order);
+                                      scale, s, e, tstart, tstop, pk, drop, bmask, order, score);
   return bwd_launch_d<256, 128, 32>(q, k, v, o, lse, dout, dq, dk, dv, workspace, B, Hq, Hkv, N, left, right,
-                                    scale, s, e, tstart, tstop, pk, drop, bmask, order);
+                                    scale, s, e, tstart, tstop, pk, drop, bmask, order, score);
 }
 
 }  // namespace fa

@@ -31,12 +31,17 @@
 //  * S^T is double-buffered in TMEM, so the tensor core computes block j+1's scores while
 //    the softmax of block j runs; K and V blocks stream through a ring of shared-memory
 //    slots filled by TMA in the order K_0, V_0, K_1, V_1, ...
+//  * Changed scores (a tanh cap, a distance bias: fa_score.cuh) are formed by the thread that
+//    owns the key right after it has loaded its scores, in both passes; the kernel stays bound
+//    by the cache's bytes.  In this variant V rows behind the last key are also cleared in
+//    shared memory, so that a cache may hold anything there (0 * NaN would reach O).
 //  * The running max is moved only when a column's max rises by more than 2^8 (log2
 //    units); the rare rescale of O^T waits for the previous block's P V.
 #pragma once
 
 #include "fa_common.cuh"
 #include "fa_fwd.cuh"
+#include "fa_score.cuh"
 
 namespace fa {
 
@@ -51,6 +56,7 @@ struct DecodeParams {
   int splits, chunk;     // split s covers keys [s * chunk, (s + 1) * chunk), chunk % 128 == 0
   int causal;
   float sl2;             // scale * log2(e)
+  ScoreCfg score;        // changed scores (SCORE kernels only; no key ranges)
 };
 
 __host__ __device__ constexpr int pow2_at_least(int x) {
@@ -131,7 +137,7 @@ __device__ __forceinline__ void st_shared_u16(uint32_t addr, uint16_t v) {
   asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
 }
 
-template <int D, int RP>
+template <int D, int RP, bool SCORE = false>
 __global__ void __launch_bounds__(kDecodeThreads, DecodeLayout<D, RP>::kCtasPerSM)
     fa_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const DecodeParams p) {
@@ -315,7 +321,7 @@ __global__ void __launch_bounds__(kDecodeThreads, DecodeLayout<D, RP>::kCtasPerS
     float *red = vec;                             // [4][RP] per-warp column maxima / sums
     float *mu = vec + 4 * RP;                     // exponent offset per column
     float *al = vec + 5 * RP;                     // rescale factor per column
-    const float sl2 = p.sl2;
+    const float sl2 = SCORE ? 1.f : p.sl2;        // changed scores are in log2 units already
     const int pos0 = len - p.Nq;                  // position of the first new token
     float l_part[RP];                             // this key's share of each row's sum
 #pragma unroll
@@ -328,6 +334,27 @@ __global__ void __launch_bounds__(kDecodeThreads, DecodeLayout<D, RP>::kCtasPerS
         tmem_ld_x16(tS + ch * CW, sc);
       else
         tmem_ld_x32(tS + ch * CW, sc);
+      if constexpr (SCORE) {
+        float none[1];
+        ScoreCfg capped = p.score;
+        capped.slopes = nullptr;
+        score_log2<CW, false, false>(sc, none, capped, p.sl2, 0.f, 0, 0, 0);
+        if (p.score.slopes) {
+          // column c is token t = c mod Nq of query head c / Nq of the group
+          const int grp = p.R / p.Nq;
+          const float *slope = p.score.slopes + kvh * grp;
+          int t = (ch * CW) % p.Nq, h = (ch * CW) / p.Nq;
+#pragma unroll
+          for (int c = 0; c < CW; ++c) {
+            const float g2 = slope[min(h, grp - 1)] * kLog2e;
+            sc[c] = __float_as_uint(fmaf(-g2, fabsf(static_cast<float>(pos0 + t - kv)), __uint_as_float(sc[c])));
+            if (++t == p.Nq) {
+              t = 0;
+              ++h;
+            }
+          }
+        }
+      }
       if (kv >= k_end) {
 #pragma unroll
         for (int c = 0; c < CW; ++c) sc[c] = __float_as_uint(-INFINITY);
@@ -427,6 +454,23 @@ __global__ void __launch_bounds__(kDecodeThreads, DecodeLayout<D, RP>::kCtasPerS
                           __bfloat16_as_ushort(pb));
           }
         }
+      }
+      if constexpr (SCORE) {
+        // The last block's V rows behind the last key: cleared once they have landed, before
+        // the P arrival that lets the tensor core read them.
+        bool landed = true;
+        if (kv >= k_end) {
+          const int slot = (2 * j + 1) % S;
+          landed = wait_bounded(bar(L::kBarKVFull + slot), ((2 * j + 1) / S) & 1, abort_flag,
+                                wait_site(4, L::kBarKVFull + slot, 2 * j + 1));
+          if (landed) {
+            const uint32_t row = sKV + slot * L::kKVTile + lk * 128;
+#pragma unroll
+            for (int u = 0; u < 8 * L::kChunks; ++u)
+              st_shared_v4(row + (u / 8) * L::kKVChunk + (u % 8) * 16, 0u, 0u, 0u, 0u);
+          }
+        }
+        ok = __all_sync(0xffffffffu, landed) && ok;  // the same for the whole warp
       }
       fence_proxy_async_smem();
       tc_fence_before_sync();

@@ -39,6 +39,7 @@
 #pragma once
 
 #include "fa_common.cuh"
+#include "fa_score.cuh"
 
 namespace fa {
 
@@ -56,6 +57,7 @@ struct FwdParams {
   const uint8_t *bmask;   // block-sparse: [B, Hq, nqb, nqb] 0/1 over 128 x 128 blocks
   int tsz;                // unit order: levels per tier (see unit_order)
   int tail;               // unit order: heads taken level by level at the end
+  ScoreCfg score;         // changed scores (kAttnScore only)
 };
 
 // Blocks of KB keys [lo, hi] that some row q0 .. min(q0 + 127, Lq - 1) of a query tile can
@@ -69,6 +71,41 @@ __device__ __forceinline__ bool key_block_range(int left, int right, const SeqGe
   if (last < first) return false;
   lo = first / KB;
   hi = last / KB;
+  return true;
+}
+
+// Changed scores: the warps of a 128-row query tile (warp wq holds rows q0 + 32 wq ..) leave in
+// `span` the smallest visible key and the end of the visible keys of its rows.
+__device__ __forceinline__ void score_tile_span(const ScoreCfg &cfg, int b, int q0, int N, int wq, int lane,
+                                                int2 *span) {
+  int lo, hi;
+  row_range(cfg, b, q0 + wq * 32 + lane, N, lo, hi);
+  if (hi <= lo) {
+    lo = INT_MAX;
+    hi = 0;
+  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lane == 0) span[wq] = make_int2(lo, hi);
+}
+
+// Blocks of KB keys [first, first + count) that the tile's rows see (count 0: none).
+template <int KB>
+__device__ __forceinline__ void score_tile_blocks(const int2 *span, int &first, int &count) {
+  const int lo = min(min(span[0].x, span[1].x), min(span[2].x, span[3].x));
+  const int hi = max(max(span[0].y, span[1].y), max(span[2].y, span[3].y));
+  first = hi > 0 ? lo / KB : 0;
+  count = hi > 0 ? (hi - 1) / KB + 1 - first : 0;
+}
+
+// Hides with -inf the scores of keys kv0 + c outside [lo, hi); true when the warp had to.
+template <int NC>
+__device__ __forceinline__ bool mask_score_range(uint32_t (&s)[NC], int lo, int hi, int kv0) {
+  const int c_lo = lo - kv0, c_hi = hi - kv0;
+  if (!__any_sync(0xffffffffu, c_lo > 0 || c_hi < NC)) return false;
+#pragma unroll
+  for (int c = 0; c < NC; ++c)
+    if (c < c_lo || c >= c_hi) s[c] = __float_as_uint(-INFINITY);
   return true;
 }
 
@@ -132,6 +169,8 @@ struct FwdLayout {
   // of tile 1} and the CTA's key-block list (uint16: block | tile-0 bit 14 | tile-1 bit 15).
   static constexpr int kOffList = kOffMisc + 16;
   static constexpr int kSmemBytesSparse = kOffList + 16 + 2 * kMaxSparseBlocks + 1024;
+  // Changed scores only: after misc, the visible-key span of each warp's rows.
+  static constexpr int kSmemBytesScore = kOffList + 2 * 4 * 8 + 1024;
   static constexpr uint32_t kTmemCols = 512;
   __host__ __device__ static constexpr uint32_t tm_s(int t) { return static_cast<uint32_t>(t) * 128u; }
   __host__ __device__ static constexpr uint32_t tm_o(int t) { return 256u + static_cast<uint32_t>(t * D); }
@@ -328,7 +367,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   const int kvh = h[0] / g;
   constexpr bool GEN = MODE == kAttnGeneral;
   constexpr bool SPARSE = MODE == kAttnSparse;
-  constexpr bool GENLIKE = GEN || SPARSE;  // rows may see no key at all
+  constexpr bool SCORE = MODE == kAttnScore;
+  constexpr bool RANGED = GEN || SCORE;    // each tile has a key-block range of its own
+  constexpr bool GENLIKE = RANGED || SPARSE;  // rows may see no key at all
   const bool packed = GEN && p.cu_q != nullptr;
   SeqGeom sg{p.N, p.N, 0, 0, 0};
   // Key blocks: the CTA walks the union [ulo, ulo + nu) of its tiles' ranges (contiguous:
@@ -352,7 +393,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     nblk[0] = has0 ? hi0 - lo0 + 1 : 0;
     a[1] = has1 ? lo1 - ulo : 0;
     nblk[1] = has1 ? hi1 - lo1 + 1 : 0;
-  } else if constexpr (!SPARSE) {
+  } else if constexpr (!SPARSE && !SCORE) {
 #pragma unroll
     for (int t = 0; t < 2; ++t) nblk[t] = !valid[t] ? 0 : (MODE == kAttnCausal ? qb[t] + 1 : p.nqb);
     nu = nblk[0] > nblk[1] ? nblk[0] : nblk[1];
@@ -416,10 +457,25 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       }
     }
   }
+  int2 *span = reinterpret_cast<int2 *>(smem + L::kOffList);  // changed scores: [tile][warp]
+  if constexpr (SCORE) {
+    if (warp < 8)
+      score_tile_span(p.score, b, (warp / 4 ? (valid[1] ? qb[1] : p.nqb) : qb[0]) * 128, p.N, warp % 4, lane,
+                      span + warp / 4 * 4);
+  }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = misc[0];
+  if constexpr (SCORE) {
+    int f0, f1;
+    score_tile_blocks<128>(span, f0, nblk[0]);
+    score_tile_blocks<128>(span + 4, f1, nblk[1]);
+    ulo = nblk[0] == 0 ? f1 : nblk[1] == 0 ? f0 : min(f0, f1);
+    a[0] = nblk[0] > 0 ? f0 - ulo : 0;
+    a[1] = nblk[1] > 0 ? f1 - ulo : 0;
+    nu = max(a[0] + nblk[0], a[1] + nblk[1]);
+  }
   if constexpr (SPARSE) {
     const int *hdr = reinterpret_cast<const int *>(smem + L::kOffList);
     nu = hdr[0];
@@ -593,7 +649,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       } else {
       // Local block range of each tile (an empty tile gets an empty range; in the dense
       // variants every tile starts at block 0).
-      const int first[2] = {!GEN ? 0 : (nblk[0] > 0 ? a[0] : 1 << 30), !GEN ? 0 : (nblk[1] > 0 ? a[1] : 1 << 30)};
+      const int first[2] = {!RANGED ? 0 : (nblk[0] > 0 ? a[0] : 1 << 30),
+                            !RANGED ? 0 : (nblk[1] > 0 ? a[1] : 1 << 30)};
       const int last[2] = {a[0] + nblk[0] - 1, a[1] + nblk[1] - 1};
       bool ok = nu > 0;
 #pragma unroll
@@ -681,7 +738,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     // much smaller rounding errors) the weights the P V product actually used, so that
     // O / r_run is a properly normalised average.
     float m_run = -INFINITY, l_run = 0.f, r_run = 0.f;
-    const float sl2 = p.sl2;
+    const float sl2 = SCORE ? 1.f : p.sl2;  // changed scores are in log2 units already
+    int row_lo = 0, row_hi = 0;
+    float slope2 = 0.f;
+    if constexpr (SCORE) {
+      row_range(p.score, b, my_valid ? qrow : p.N, p.N, row_lo, row_hi);
+      if (p.score.slopes) slope2 = p.score.slopes[my_h] * kLog2e;
+    }
     // Block-sparse: this tile's current entry of the block list, and the number of score
     // tiles (both tiles) listed before it, which gives the block's S buffer and phase.
     int cur = -1, nbase = 0, prev_bits = 0, uses0 = 0, uses1 = 0;  // uses: own blocks per buffer
@@ -721,6 +784,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       if constexpr (GEN) {
         masked = block_needs_mask<128>(p.left, p.right, sg.Lk, my_qb * 128 + sg.dlt, kv0);
         if (masked) mask_scores<128>(s, p.left, p.right, sg.Lk, qrow + sg.dlt, kv0);
+      } else if constexpr (SCORE) {
+        const int side = kv0 + 127 <= my_qb * 128 ? -1 : (kv0 >= my_qb * 128 + 127 ? 1 : 0);
+        float none[1];
+        score_log2<128, false>(s, none, p.score, p.sl2, slope2, qrow, kv0, side);
+        masked = mask_score_range<128>(s, row_lo, row_hi, kv0);
       } else {
         const bool causal = MODE == kAttnCausal || (SPARSE && p.right == 0);
         masked = (causal && kv0 == my_qb * 128) || kv0 + 128 > p.N;
@@ -734,10 +802,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const float smax = row_max128(s);
       const float m_cand = smax * sl2;
       const float m_new = (m_cand > m_run + kRescaleThreshold) ? m_cand : m_run;
-      // 0 on a row's first visible block, else <= 1.  A band can hide a whole block from
-      // a row; while its max is still -inf the offset stays 0 and alpha 1 (no inf - inf).
-      const float alpha = (GEN && m_new == m_run) ? 1.f : ex2_approx(m_run - m_new);
-      const float m_use = (GEN && m_new == -INFINITY) ? 0.f : m_new;
+      // 0 on a row's first visible block, else <= 1.  A band or range can hide a whole block
+      // from a row; while its max is still -inf the offset stays 0 and alpha 1 (no inf - inf).
+      const float alpha = (RANGED && m_new == m_run) ? 1.f : ex2_approx(m_run - m_new);
+      const float m_use = (RANGED && m_new == -INFINITY) ? 0.f : m_new;
       float lsum, ppmax;
       if (masked)
         exp_block<128, false, DROP>(s, sl2, m_use, tS, lsum, ppmax, p.drop, kv0 >> 3, qrow,
@@ -789,7 +857,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       if (okw && (!GENLIKE || (!direct && my_n > 0))) {
         tc_fence_after_sync();
         // rows without keys: O = 0; dropout scales the kept probabilities by 1 / (1 - p)
-        const float inv_l = (!GEN || r_run > 0.f) ? (DROP ? p.drop.inv_keep : 1.f) / r_run : 0.f;
+        const float inv_l = (!RANGED || r_run > 0.f) ? (DROP ? p.drop.inv_keep : 1.f) / r_run : 0.f;
         const uint32_t stage = sQ + t * L::kTileBytes;
 #pragma unroll
         for (int cc = 0; cc < D / 32; ++cc) {

@@ -52,6 +52,8 @@ struct FwdD256Layout {
   // 64-key blocks to visit (uint16), two per enabled 128-key mask block.
   static constexpr int kOffList = kOffMisc + 16;
   static constexpr int kSmemBytesSparse = kOffList + 16 + 2 * (2 * kMaxSparseBlocks) + 1024;
+  // Changed scores only: after misc, the visible-key span of each warp's rows.
+  static constexpr int kSmemBytesScore = kOffList + 4 * 8 + 1024;
   static constexpr uint32_t kTmemCols = 512;
   static constexpr uint32_t kTmS0 = 0;     // S_a: columns 0..63, S_b: 64..127
   static constexpr uint32_t kTmO = 128;    // O: columns 128..383
@@ -90,7 +92,9 @@ __global__ void __launch_bounds__(kFwdD256Threads, 1)
   const int kvh = h / (p.Hq / p.Hkv);
   constexpr bool GEN = MODE == kAttnGeneral;
   constexpr bool SPARSE = MODE == kAttnSparse;
-  constexpr bool GENLIKE = GEN || SPARSE;  // rows may see no key at all
+  constexpr bool SCORE = MODE == kAttnScore;
+  constexpr bool RANGED = GEN || SCORE;
+  constexpr bool GENLIKE = RANGED || SPARSE;  // rows may see no key at all
   const bool packed = GEN && p.cu_q != nullptr;
   // Block-sparse: the 64-key blocks of the enabled 128-key mask blocks of this query block
   // (up to the diagonal when causal), in order; written to shared memory by the TMA warp
@@ -106,7 +110,7 @@ __global__ void __launch_bounds__(kFwdD256Threads, 1)
     int jhi = -1;
     key_block_range<64>(p.left, p.right, sg, qb * 128, jlo, jhi);
     nblk = jhi - jlo + 1;
-  } else if constexpr (!SPARSE) {
+  } else if constexpr (!SPARSE && !SCORE) {
     const int nkb_all = (p.N + 63) / 64;
     nblk = MODE == kAttnCausal ? min(2 * qb + 2, nkb_all) : nkb_all;
   }
@@ -148,10 +152,15 @@ __global__ void __launch_bounds__(kFwdD256Threads, 1)
       if (lane == 0) *reinterpret_cast<int *>(smem + L::kOffList) = n;
     }
   }
+  int2 *span = reinterpret_cast<int2 *>(smem + L::kOffList);  // changed scores: [warp]
+  if constexpr (SCORE) {
+    if (warp < 4) score_tile_span(p.score, b, qb * 128, p.N, warp, lane, span);
+  }
   tc_fence_before_sync();
   __syncthreads();
   tc_fence_after_sync();
   const uint32_t tmem = misc[0];
+  if constexpr (SCORE) score_tile_blocks<64>(span, jlo, nblk);
   if constexpr (SPARSE) nblk = *reinterpret_cast<const int *>(smem + L::kOffList);
 
   // Load/consume order of the K/V ring: K_0, K_1, then V_j followed by K_{j+2}.
@@ -268,7 +277,13 @@ __global__ void __launch_bounds__(kFwdD256Threads, 1)
     // l_run: sum of the fp32 probabilities (for the LSE); r_run: the same with each
     // block's largest probability counted as rounded to bf16 (see pmax_rounding).
     float m_run = -INFINITY, l_run = 0.f, r_run = 0.f;
-    const float sl2 = p.sl2;
+    const float sl2 = SCORE ? 1.f : p.sl2;  // changed scores are in log2 units already
+    int row_lo = 0, row_hi = 0;
+    float slope2 = 0.f;
+    if constexpr (SCORE) {
+      row_range(p.score, b, qrow, p.N, row_lo, row_hi);
+      if (p.score.slopes) slope2 = p.score.slopes[h] * kLog2e;
+    }
     for (int j = 0; ok && j < nblk; ++j) {
       const uint32_t tS = tmem + L::kTmS0 + (j & 1) * 64 + lane_off;
       if (!warp_wait_bounded(bar(L::kBarS + (j & 1)), (j >> 1) & 1, abort_flag,
@@ -284,6 +299,11 @@ __global__ void __launch_bounds__(kFwdD256Threads, 1)
       if constexpr (GEN) {
         masked = block_needs_mask<64>(p.left, p.right, sg.Lk, qb * 128 + sg.dlt, kv0);
         if (masked) mask_scores<64>(s, p.left, p.right, sg.Lk, qrow + sg.dlt, kv0);
+      } else if constexpr (SCORE) {
+        const int side = kv0 + 63 <= qb * 128 ? -1 : (kv0 >= qb * 128 + 127 ? 1 : 0);
+        float none[1];
+        score_log2<64, false>(s, none, p.score, p.sl2, slope2, qrow, kv0, side);
+        masked = mask_score_range<64>(s, row_lo, row_hi, kv0);
       } else {
         // (block-sparse: a row's first block always holds a visible key, the diagonal
         // block's first half coming before its second)
@@ -301,8 +321,8 @@ __global__ void __launch_bounds__(kFwdD256Threads, 1)
       const float m_new = (m_cand > m_run + kRescaleThreshold) ? m_cand : m_run;
       // A band can hide a whole block from a row: while its max is still -inf the offset
       // stays 0 and alpha 1.
-      const float alpha = (GEN && m_new == m_run) ? 1.f : ex2_approx(m_run - m_new);
-      const float m_use = (GEN && m_new == -INFINITY) ? 0.f : m_new;
+      const float alpha = (RANGED && m_new == m_run) ? 1.f : ex2_approx(m_run - m_new);
+      const float m_use = (RANGED && m_new == -INFINITY) ? 0.f : m_new;
       float lsum, ppmax;
       if (masked)
         exp_block<64, false, DROP>(s, sl2, m_use, tS, lsum, ppmax, p.drop, kv0 >> 3, qrow, b * p.Hq + h);

@@ -1,0 +1,172 @@
+// fa_score.cuh - scores that are changed before the softmax: capped by a tanh, lowered with
+// the distance between query and key, or hidden outside a key range of the query's own.
+//
+// For query i and key j of head h, with x = scale q_i . k_j:
+//   y = cap tanh(x / cap)   (cap = 0: y = x),      s_ij = y - slope_h |i - j|,
+// and key j is visible to query i iff lo_i <= j < hi_i (and j <= i when causal).  Documents
+// packed into one row, visible prefixes, padding and their combinations are such ranges.
+// The kernels work in units of log2: s_ij log2(e).
+//
+// The gradient: with t = tanh(x / cap), d s_ij / d x = 1 - t^2; the bias is a constant.
+//
+// tanh.  MUFU.TANH is off by 2^-11 of its value: at cap = 50 a score of 20 would be off by
+// 0.01 and its probability by 1%.  Two forms take its place, chosen per warp and block by
+// the largest |x| / cap in it:
+//  * up to 0.7: t = u P(u^2), P of degree 4, this library's own minimax fit of the relative
+//    error of tanh(u) / u (3.1e-7), two scores per FMA-pipe instruction;
+//  * beyond: t = sign(u) (1 - w) / (1 + w), w = 2^(-2 log2(e) |u|): two MUFU operations; the
+//    absolute error stays below 2^-21, whatever u.  1 - t^2 is then 4 w / (1 + w)^2, which
+//    keeps its relative accuracy where t is near 1 (1 - t t would be all rounding there).
+#pragma once
+
+#include "fa_common.cuh"
+
+namespace fa {
+
+struct ScoreCfg {
+  float cap_in;         // scale / cap (0: no cap)
+  float cap_log2;       // cap * log2(e)
+  const float *slopes;  // [Hq] or nullptr
+  const int2 *range;    // [B, N] (lo, hi) or nullptr
+  int causal;
+};
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kTanhPolyMax = 0.7f;
+constexpr float kTanhC0 = 0.9999997019767761f, kTanhC1 = -0.3333021402359009f, kTanhC2 = 0.13281112909317017f, kTanhC3 = -0.0508362352848053f, kTanhC4 = 0.01377371046692133f;
+
+// tanh of a pair, |u| <= kTanhPolyMax.
+__device__ __forceinline__ uint64_t f2_tanh_poly(uint64_t u) {
+  const uint64_t z = f2_mul(u, u);
+  uint64_t q = f2_fma(f2_pack(kTanhC4, kTanhC4), z, f2_pack(kTanhC3, kTanhC3));
+  q = f2_fma(q, z, f2_pack(kTanhC2, kTanhC2));
+  q = f2_fma(q, z, f2_pack(kTanhC1, kTanhC1));
+  q = f2_fma(q, z, f2_pack(kTanhC0, kTanhC0));
+  return f2_mul(q, u);
+}
+
+// tanh of any u, and 1 - tanh^2.
+__device__ __forceinline__ float tanh_any(float u, float &grad) {
+  const float w = ex2_approx(fabsf(u) * (-2.f * kLog2e));
+  const float r = __fdividef(1.f, 1.f + w);
+  grad = 4.f * w * r * r;
+  return copysignf((1.f - w) * r, u);
+}
+
+// The visible keys of query row i (hi <= lo: none).
+__device__ __forceinline__ void row_range(const ScoreCfg &c, int b, int i, int N, int &lo, int &hi) {
+  lo = 0;
+  hi = N;
+  if (i >= N) {
+    hi = 0;
+    return;
+  }
+  if (c.range) {
+    const int2 r = c.range[static_cast<size_t>(b) * N + i];
+    lo = max(r.x, 0);
+    hi = min(r.y, N);
+  }
+  if (c.causal) hi = min(hi, i + 1);
+}
+
+// Largest |s| of N raw scores.
+template <int N>
+__device__ __forceinline__ float row_absmax(const uint32_t (&s)[N]) {
+  float m0 = 0.f, m1 = 0.f;
+#pragma unroll
+  for (int c = 0; c < N; c += 4) {
+    m0 = fmax3(m0, fabsf(__uint_as_float(s[c + 0])), fabsf(__uint_as_float(s[c + 1])));
+    m1 = fmax3(m1, fabsf(__uint_as_float(s[c + 2])), fabsf(__uint_as_float(s[c + 3])));
+  }
+  return fmaxf(m0, m1);
+}
+
+// Turns the raw products s[c] = q . k of one fixed index (row or key) `at` with N consecutive
+// others `first` + c into scores in log2 units, in place.  `side`: -1 when every other index
+// is <= at, +1 when every one is >= at, 0 otherwise (the same for the whole warp).  With GRAD
+// and a cap, grad[c] = 1 - tanh^2.  POLY = false leaves the polynomial form out.
+template <int N, bool GRAD, bool POLY = true>
+__device__ __forceinline__ void score_log2(uint32_t (&s)[N], float (&grad)[GRAD ? N : 1], const ScoreCfg &cfg,
+                                           float sl2, float slope2, int at, int first, int side) {
+  if (cfg.cap_in > 0.f) {
+    bool poly = false;
+    if constexpr (POLY) poly = __all_sync(0xffffffffu, row_absmax<N>(s) * cfg.cap_in <= kTanhPolyMax);
+    if (poly) {
+      const uint64_t in2 = f2_pack(cfg.cap_in, cfg.cap_in), out2 = f2_pack(cfg.cap_log2, cfg.cap_log2);
+#pragma unroll
+      for (int c = 0; c < N; c += 2) {
+        const uint64_t u = f2_mul(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), in2);
+        const uint64_t t = f2_tanh_poly(u);
+        float a, b;
+        f2_unpack(f2_mul(t, out2), a, b);
+        s[c] = __float_as_uint(a);
+        s[c + 1] = __float_as_uint(b);
+        if constexpr (GRAD)
+          f2_unpack(f2_fma(f2_mul(t, f2_pack(-1.f, -1.f)), t, f2_pack(1.f, 1.f)), grad[c], grad[c + 1]);
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < N; ++c) {
+        float slope;
+        s[c] = __float_as_uint(cfg.cap_log2 * tanh_any(__uint_as_float(s[c]) * cfg.cap_in, slope));
+        if constexpr (GRAD) grad[c] = slope;
+      }
+    }
+  } else {
+    const uint64_t k2 = f2_pack(sl2, sl2);
+#pragma unroll
+    for (int c = 0; c < N; c += 2) {
+      float a, b;
+      f2_unpack(f2_mul(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), k2), a, b);
+      s[c] = __float_as_uint(a);
+      s[c + 1] = __float_as_uint(b);
+    }
+  }
+  if (cfg.slopes) {
+    if (side != 0) {
+      // -slope |at - (first + c)| = g c + g (first - at), g = slope below `at`, -slope above
+      const float g = side < 0 ? slope2 : -slope2;
+      const float base = g * static_cast<float>(first - at);
+      const uint64_t g2 = f2_pack(g, g), b2 = f2_pack(base, base);
+#pragma unroll
+      for (int c = 0; c < N; c += 2) {
+        const uint64_t bias = f2_fma(f2_pack(static_cast<float>(c), static_cast<float>(c + 1)), g2, b2);
+        float a, b;
+        f2_unpack(f2_add(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), bias), a, b);
+        s[c] = __float_as_uint(a);
+        s[c + 1] = __float_as_uint(b);
+      }
+    } else {
+      const float d0 = static_cast<float>(first - at);
+#pragma unroll
+      for (int c = 0; c < N; ++c)
+        s[c] = __float_as_uint(fmaf(-slope2, fabsf(d0 + static_cast<float>(c)), __uint_as_float(s[c])));
+    }
+  }
+}
+
+// Smallest lo and largest hi over the rows of each 128-row query block that see a key
+// ((INT_MAX, 0) when none does): the backward's key blocks pick their query blocks by it.
+__global__ void __launch_bounds__(128) fa_score_blocks_kernel(const ScoreCfg cfg, int N, int2 *blocks) {
+  __shared__ int red[2][4];
+  const int qb = blockIdx.x, b = blockIdx.y;
+  int lo, hi;
+  row_range(cfg, b, qb * 128 + static_cast<int>(threadIdx.x), N, lo, hi);
+  if (hi <= lo) {
+    lo = INT_MAX;
+    hi = 0;
+  }
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (threadIdx.x % 32 == 0) {
+    red[0][threadIdx.x / 32] = lo;
+    red[1][threadIdx.x / 32] = hi;
+  }
+  __syncthreads();
+  if (threadIdx.x == 0)
+    blocks[static_cast<size_t>(b) * gridDim.x + qb] =
+        make_int2(min(min(red[0][0], red[0][1]), min(red[0][2], red[0][3])),
+                  max(max(red[1][0], red[1][1]), max(red[1][2], red[1][3])));
+}
+
+}  // namespace fa

@@ -22,7 +22,13 @@ Entry points mirror the C ABI names:
 * :func:`fwd` / :func:`bwd` / :func:`fwd_varlen` / :func:`bwd_varlen` / :func:`decode` /
   :func:`merge` - tensor conveniences that allocate outputs with torch
   (``window=(left, right)`` selects local attention, ``dropout_p`` / ``seed`` dropout,
-  ``block_mask`` block-sparse attention);
+  ``block_mask`` block-sparse attention; ``softcap``, ``alibi_slopes``, ``key_range`` changed
+  scores);
+* :func:`fa_fwd_score` / :func:`fa_bwd_score` / :func:`fa_decode_score` - attention with
+  changed scores: a tanh cap, a bias that falls with the distance, a key range per query row
+  (:func:`document_ranges`, :func:`prefix_ranges`);
+* :func:`kv4_alloc` / :func:`kv4_write` / :func:`kv4_read` / :func:`decode_kv4` - a key/value
+  cache held in 4 bits: allocated, written, read back, attended to;
 * :func:`fa_bwd_workspace_bytes`, :func:`fa_device_status`, :func:`fa_status_string`.
 """
 from __future__ import annotations
@@ -109,6 +115,16 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.fa_decode.argtypes = [vp, vp, vp, vp, vp, vp, vp, sz, ci, ci, ci, ci, ci, ci, ci, ci,
                                   cf, vp]
         lib.fa_decode.restype = ci
+        lib.fa_fwd_score.argtypes = [vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, ci, cf, cf, vp]
+        lib.fa_fwd_score.restype = ci
+        lib.fa_bwd_score_workspace_bytes.argtypes = [ci, ci, ci, ci, ci]
+        lib.fa_bwd_score_workspace_bytes.restype = sz
+        lib.fa_bwd_score.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, vp, vp, sz, vp, vp, ci, ci, ci,
+                                     ci, ci, ci, cf, cf, vp]
+        lib.fa_bwd_score.restype = ci
+        lib.fa_decode_score.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, sz, ci, ci, ci, ci, ci, ci,
+                                        ci, ci, cf, cf, vp]
+        lib.fa_decode_score.restype = ci
         lib.fa_kv4_write.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, vp]
         lib.fa_kv4_write.restype = ci
         lib.fa_kv4_read.argtypes = [vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, vp]
@@ -259,6 +275,31 @@ def fa_decode(q, k, v, o, lse, seqlens_k, workspace, workspace_bytes, B, Hq, Hkv
            "fa_decode")
 
 
+def fa_fwd_score(q, k, v, o, lse, alibi_slopes, key_range, B, Hq, Hkv, N, d, causal, softcap, scale,
+                 stream) -> None:
+    _check(load().fa_fwd_score(q, k, v, o, lse, alibi_slopes, key_range, B, Hq, Hkv, N, d,
+                               int(causal), float(softcap), float(scale), stream), "fa_fwd_score")
+
+
+def fa_bwd_score_workspace_bytes(B, Hq, Hkv, N, d) -> int:
+    return int(load().fa_bwd_score_workspace_bytes(B, Hq, Hkv, N, d))
+
+
+def fa_bwd_score(q, k, v, o, lse, dout, dq, dk, dv, workspace, workspace_bytes, alibi_slopes,
+                 key_range, B, Hq, Hkv, N, d, causal, softcap, scale, stream) -> None:
+    _check(load().fa_bwd_score(q, k, v, o, lse, dout, dq, dk, dv, workspace, workspace_bytes,
+                               alibi_slopes, key_range, B, Hq, Hkv, N, d, int(causal),
+                               float(softcap), float(scale), stream), "fa_bwd_score")
+
+
+def fa_decode_score(q, k, v, o, lse, seqlens_k, alibi_slopes, workspace, workspace_bytes, B, Hq,
+                    Hkv, Nq, Nk, d, causal, num_splits, softcap, scale, stream) -> None:
+    _check(load().fa_decode_score(q, k, v, o, lse, seqlens_k, alibi_slopes, workspace,
+                                  workspace_bytes, B, Hq, Hkv, Nq, Nk, d, int(causal),
+                                  int(num_splits), float(softcap), float(scale), stream),
+           "fa_decode_score")
+
+
 def fa_kv4_write(k, v, k_codes, k_params, v_codes, v_params, start, counts, B, Hkv, n, cap, d,
                  stream) -> None:
     _check(load().fa_kv4_write(k, v, k_codes, k_params, v_codes, v_params, start, counts, B, Hkv,
@@ -379,14 +420,79 @@ def _block_mask(block_mask, B, Hq, N, win, dropout_p):
     return block_mask
 
 
+def _int32_vector(t, name, B, device):
+    """Device pointer of an int32 [B] tensor (None stays None)."""
+    import torch
+    if t is None:
+        return None
+    if (not t.is_cuda or t.dtype != torch.int32 or tuple(t.shape) != (B,) or not t.is_contiguous()
+            or t.device != device):
+        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of B = {B} entries on {device}")
+    return t.data_ptr()
+
+
+def _slopes(alibi_slopes, Hq, device):
+    """Device pointer of the fp32 [Hq] distance slopes (None stays None)."""
+    import torch
+    if alibi_slopes is None:
+        return None
+    if (not alibi_slopes.is_cuda or alibi_slopes.dtype != torch.float32 or alibi_slopes.device != device
+            or tuple(alibi_slopes.shape) != (Hq,) or not alibi_slopes.is_contiguous()):
+        raise ValueError(f"alibi_slopes must be a contiguous fp32 CUDA tensor of Hq = {Hq} entries on {device}")
+    return alibi_slopes.data_ptr()
+
+
+def _same_device(first, *others):
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"all tensors must be on one device ({t.device} is not {first.device})")
+
+
+def _out(t, name, shape, dtype, like):
+    """`t`, checked to be a tensor of that shape on like's device, or a new one."""
+    import torch
+    if t is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    if not t.is_cuda or t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor {list(shape)}")
+    _same_device(like, t)
+    return t
+
+
+def _key_range(key_range, B, N, device):
+    """Device pointer of the int32 [B, N, 2] key ranges (None stays None)."""
+    import torch
+    if key_range is None:
+        return None
+    if (not key_range.is_cuda or key_range.dtype != torch.int32 or key_range.device != device
+            or tuple(key_range.shape) != (B, N, 2) or not key_range.is_contiguous()):
+        raise ValueError(f"key_range must be a contiguous int32 CUDA tensor [{B}, {N}, 2] on {device}")
+    return key_range.data_ptr()
+
+
+def _changes_scores(softcap, alibi_slopes, key_range=None):
+    return bool(softcap) or alibi_slopes is not None or key_range is not None
+
+
+def _score_alone(win, dropout_p, block_mask):
+    if win is not None or dropout_p or block_mask is not None:
+        raise ValueError("softcap, alibi_slopes and key_range combine with causal only "
+                         "(no window, dropout or block_mask; a window is a key_range)")
+
+
 def fwd(q, k, v, causal: bool = False, scale: float | None = None, out=None, lse=None,
-        window=None, dropout_p: float = 0.0, seed: int = 0, block_mask=None):
+        window=None, dropout_p: float = 0.0, seed: int = 0, block_mask=None, softcap: float = 0.0,
+        alibi_slopes=None, key_range=None):
     """O, LSE = attention(q, k, v); q [B,Hq,N,d], k/v [B,Hkv,N,d] bf16 on one GPU.
     ``window=(left, right)``: local attention, key j visible to query i iff
     i - left <= j <= i + right (-1 = unlimited on that side).  ``dropout_p`` > 0: attention
     dropout with the Philox4x32-10 mask of ``seed`` (full or causal attention).
     ``block_mask``: block-sparse attention, uint8 (or bool) [B, Hq, ceil(N/128), ceil(N/128)]
-    on the GPU, nonzero = the 128 x 128 block is computed (with or without ``causal``)."""
+    on the GPU, nonzero = the 128 x 128 block is computed (with or without ``causal``).
+    Changed scores (with or without ``causal``): ``softcap`` c > 0 makes each scaled score x
+    c tanh(x / c); ``alibi_slopes`` fp32 [Hq] takes slope |i - j| off; ``key_range`` int32
+    [B, N, 2] gives the keys lo <= j < hi that each query row sees (see document_ranges and
+    prefix_ranges); a row without keys gets O = 0 and LSE = -inf."""
     import torch
     win = _window(causal, window)
     for t, n in ((q, "q"), (k, "k"), (v, "v")):
@@ -397,6 +503,16 @@ def fwd(q, k, v, causal: bool = False, scale: float | None = None, out=None, lse
     scale = default_scale(d) if scale is None else scale
     o = torch.empty_like(q) if out is None else out
     l = torch.empty((B, Hq, N), dtype=torch.float32, device=q.device) if lse is None else lse
+    if _changes_scores(softcap, alibi_slopes, key_range):
+        _score_alone(win, dropout_p, block_mask)
+        _same_device(q, k, v)
+        _out(o, "out", q.shape, torch.bfloat16, q)
+        _out(l, "lse", (B, Hq, N), torch.float32, q)
+        with torch.cuda.device(q.device):
+            fa_fwd_score(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), l.data_ptr(),
+                         _slopes(alibi_slopes, Hq, q.device), _key_range(key_range, B, N, q.device),
+                         B, Hq, Hkv, N, d, causal, softcap, scale, _stream_handle(q))
+        return o, l
     bm = _block_mask(block_mask, B, Hq, N, win, dropout_p)
     if bm is not None:
         fa_fwd_blocksparse(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), l.data_ptr(),
@@ -417,16 +533,18 @@ def fwd(q, k, v, causal: bool = False, scale: float | None = None, out=None, lse
 
 def bwd(q, k, v, o, lse, dout, causal: bool = False, scale: float | None = None,
         workspace=None, dq=None, dk=None, dv=None, window=None, dropout_p: float = 0.0,
-        seed: int = 0, block_mask=None):
+        seed: int = 0, block_mask=None, softcap: float = 0.0, alibi_slopes=None, key_range=None):
     """dQ, dK, dV of <O, dO> given the forward's O and LSE (same causal / window /
-    dropout / block_mask)."""
+    dropout / block_mask / softcap / alibi_slopes / key_range; the last two are constants
+    without a gradient)."""
     import torch
     win = _window(causal, window)
     for t, n in ((q, "q"), (k, "k"), (v, "v"), (o, "o"), (dout, "dout")):
         _need(t, n)
     B, Hq, Hkv, N, d = _dims(q, k)
     scale = default_scale(d) if scale is None else scale
-    nbytes = fa_bwd_workspace_bytes(B, Hq, Hkv, N, d)
+    score = _changes_scores(softcap, alibi_slopes, key_range)
+    nbytes = (fa_bwd_score_workspace_bytes if score else fa_bwd_workspace_bytes)(B, Hq, Hkv, N, d)
     if workspace is None:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
     dq = torch.empty_like(q) if dq is None else dq
@@ -435,6 +553,17 @@ def bwd(q, k, v, o, lse, dout, causal: bool = False, scale: float | None = None,
     ptrs = (q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), lse.data_ptr(),
             dout.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(),
             workspace.numel() * workspace.element_size(), B, Hq, Hkv, N, d)
+    if score:
+        _score_alone(win, dropout_p, block_mask)
+        _same_device(q, k, workspace)
+        for t, n, like in ((v, "v", k), (o, "o", q), (dout, "dout", q), (dq, "dq", q), (dk, "dk", k), (dv, "dv", k)):
+            _out(t, n, like.shape, torch.bfloat16, q)
+        _out(lse, "lse", (B, Hq, N), torch.float32, q)
+        with torch.cuda.device(q.device):
+            fa_bwd_score(*ptrs[:11], _slopes(alibi_slopes, Hq, q.device),
+                         _key_range(key_range, B, N, q.device), *ptrs[11:], causal, softcap, scale,
+                         _stream_handle(q))
+        return dq, dk, dv
     bm = _block_mask(block_mask, B, Hq, N, win, dropout_p)
     if bm is not None:
         fa_bwd_blocksparse(*ptrs[:11], bm.data_ptr(), *ptrs[11:], causal, scale, _stream_handle(q))
@@ -450,11 +579,13 @@ def bwd(q, k, v, o, lse, dout, causal: bool = False, scale: float | None = None,
 
 
 def decode(q, k, v, seqlens_k=None, causal: bool = False, scale: float | None = None,
-           num_splits: int | None = None, out=None, lse=None, workspace=None):
+           num_splits: int | None = None, out=None, lse=None, workspace=None, softcap: float = 0.0,
+           alibi_slopes=None):
     """Attention of q [B, Hq, Nq, d] against a cache k, v [B, Hkv, Nk, d] (bf16, one GPU),
     of which the first seqlens_k[b] keys are valid (int32 [B] on the GPU, or None: all).
-    Causal: the Nq queries are the last Nq positions.  Returns (O, LSE); rows that see
-    no key get O = 0 and LSE = -inf."""
+    Causal: the Nq queries are the last Nq positions.  ``softcap`` and ``alibi_slopes`` change
+    the scores as in fwd, the new rows at the last Nq positions.  Returns (O, LSE); rows that
+    see no key get O = 0 and LSE = -inf."""
     import torch
     for t, n in ((q, "q"), (k, "k"), (v, "v")):
         _need(t, n)
@@ -482,10 +613,42 @@ def decode(q, k, v, seqlens_k=None, causal: bool = False, scale: float | None = 
     l = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device) if lse is None else lse
     ws_ptr = None if workspace is None else workspace.data_ptr()
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    if _changes_scores(softcap, alibi_slopes):
+        _same_device(q, k, v, seqlens_k, workspace)
+        _out(o, "out", q.shape, torch.bfloat16, q)
+        _out(l, "lse", (B, Hq, Nq), torch.float32, q)
+        with torch.cuda.device(q.device):
+            fa_decode_score(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), l.data_ptr(), lens_ptr,
+                            _slopes(alibi_slopes, Hq, q.device), ws_ptr, ws_bytes, B, Hq, Hkv, Nq, Nk, d,
+                            causal, num_splits, softcap, scale, _stream_handle(q))
+        return o, l
     fa_decode(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), l.data_ptr(), lens_ptr,
               ws_ptr, ws_bytes, B, Hq, Hkv, Nq, Nk, d, causal, num_splits, scale,
               _stream_handle(q))
     return o, l
+
+
+def document_ranges(cu_seqlens, N: int):
+    """key_range [B, N, 2] of rows packed with documents: cu_seqlens int32 or int64 [B, D + 1],
+    the ascending offsets of the D documents of each row (repeat the last one for rows with
+    fewer).  Positions outside every document see no key."""
+    import torch
+    pos = torch.arange(N, device=cu_seqlens.device)
+    at = torch.searchsorted(cu_seqlens.contiguous(), pos.to(cu_seqlens.dtype).repeat(cu_seqlens.shape[0], 1),
+                            right=True)
+    inside = (at > 0) & (at < cu_seqlens.shape[1])
+    end = at.clamp(1, cu_seqlens.shape[1] - 1)
+    lo = torch.where(inside, cu_seqlens.gather(1, end - 1), torch.zeros_like(cu_seqlens[:, :1]))
+    hi = torch.where(inside, cu_seqlens.gather(1, end), torch.zeros_like(cu_seqlens[:, :1]))
+    return torch.stack((lo, hi), -1).to(torch.int32)
+
+
+def prefix_ranges(prefix_lens, N: int):
+    """key_range [B, N, 2] of rows whose first prefix_lens[b] keys are visible to every query and
+    the others causally (call without ``causal``)."""
+    import torch
+    hi = torch.maximum(torch.arange(1, N + 1, device=prefix_lens.device), prefix_lens[:, None]).clamp(max=N)
+    return torch.stack((torch.zeros_like(hi), hi), -1).to(torch.int32)
 
 
 #: A key/value cache held in 4 bits (see fa_kv4_write in include/fa.h for the format):
@@ -520,45 +683,6 @@ def _kv4(cache):
                 or tuple(t.shape) != (B, Hkv, cap, last)):
             raise ValueError(f"{n} must be a contiguous {dt} CUDA tensor [{B}, {Hkv}, {cap}, {last}]")
     return B, Hkv, cap, d
-
-
-def _int32_vector(t, name, B, device):
-    """Device pointer of an int32 [B] tensor (None stays None)."""
-    import torch
-    if t is None:
-        return None
-    if (not t.is_cuda or t.dtype != torch.int32 or tuple(t.shape) != (B,) or not t.is_contiguous()
-            or t.device != device):
-        raise ValueError(f"{name} must be a contiguous int32 CUDA tensor of B = {B} entries on {device}")
-    return t.data_ptr()
-
-
-def _slopes(alibi_slopes, Hq, device):
-    """Device pointer of the fp32 [Hq] distance slopes (None stays None)."""
-    import torch
-    if alibi_slopes is None:
-        return None
-    if (not alibi_slopes.is_cuda or alibi_slopes.dtype != torch.float32 or alibi_slopes.device != device
-            or tuple(alibi_slopes.shape) != (Hq,) or not alibi_slopes.is_contiguous()):
-        raise ValueError(f"alibi_slopes must be a contiguous fp32 CUDA tensor of Hq = {Hq} entries on {device}")
-    return alibi_slopes.data_ptr()
-
-
-def _same_device(first, *others):
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"all tensors must be on one device ({t.device} is not {first.device})")
-
-
-def _out(t, name, shape, dtype, like):
-    """`t`, checked to be an output tensor of that shape, or a new one."""
-    import torch
-    if t is None:
-        return torch.empty(shape, dtype=dtype, device=like.device)
-    if not t.is_cuda or t.dtype != dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} CUDA tensor {list(shape)}")
-    _same_device(like, t)
-    return t
 
 
 def kv4_write(cache, k, v, start=None, counts=None) -> None:

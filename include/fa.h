@@ -240,6 +240,46 @@ int fa_bwd_blocksparse(const void *q, const void *k, const void *v, const void *
                        void *stream);
 
 /*
+ * Attention with changed scores.  The pages name masking among the memory-bound steps of
+ * standard attention without defining masks or score functions; this library's reading, for
+ * query i and key j of query head h with x = scale * q_i . k_j:
+ *     s_ij = softcap * tanh(x / softcap) - slope[h] * |i - j|,
+ *     O_i = sum_j softmax_j(s_ij) v_j,  LSE_i = ln sum_j exp(s_ij)
+ * over the keys lo_i <= j < hi_i (with causal = 1 also j <= i).
+ *   softcap: 0 (scores as they are) or a finite c > 0.
+ *   alibi_slopes: DEVICE fp32 [Hq] (4-byte aligned), or NULL for no bias.
+ *   key_range: DEVICE int32 [B, N, 2] (8-byte aligned), (lo_i, hi_i) of every query row of a
+ *        batch entry, the same for all heads, or NULL for 0, N; values are clamped to 0 .. N.
+ *        Packed documents, visible prefixes, padding and windows are such ranges, and so is
+ *        what several of them leave.  A row with hi <= lo gets O = 0 and LSE = -inf.
+ *   q, k, v, o, lse, B, Hq, Hkv, N, d, causal, scale, stream: as fa_fwd.
+ * Key blocks (of 128, 64 for d = 256) that lie outside the ranges of all 128 rows of a query
+ * block are neither loaded nor multiplied.  Every row of K and V must hold finite values,
+ * also those that no query sees (0 * NaN is NaN in the products).
+ */
+int fa_fwd_score(const void *q, const void *k, const void *v, void *o, float *lse,
+                 const float *alibi_slopes, const int *key_range, int B, int Hq, int Hkv, int N,
+                 int d, int causal, float softcap, float scale, void *stream);
+
+/* Scratch bytes fa_bwd_score needs: those of fa_bwd and 8 bytes per batch entry and 128 query
+ * rows, padded to 256.  0 for invalid sizes. */
+size_t fa_bwd_score_workspace_bytes(int B, int Hq, int Hkv, int N, int d);
+
+/*
+ * Backward pass of fa_fwd_score (same softcap, slopes, ranges and causal flag; O and LSE from
+ * it): arguments as fa_bwd otherwise.  dS = P (dP - Delta) (1 - tanh^2(x / softcap)).  The
+ * slopes and ranges are constants: they get no gradient.  Keys that no query sees get
+ * dK = dV = 0, rows without keys dQ = 0.  Limits: B <= 65535; N below about 8 million
+ * (d = 64, 128) or 900 thousand (d = 256) rows, by the bitmap of query blocks in shared memory
+ * (FA_ERR_UNSUPPORTED beyond).
+ */
+int fa_bwd_score(const void *q, const void *k, const void *v, const void *o, const float *lse,
+                 const void *dout, void *dq, void *dk, void *dv, void *workspace,
+                 size_t workspace_bytes, const float *alibi_slopes, const int *key_range, int B,
+                 int Hq, int Hkv, int N, int d, int causal, float softcap, float scale,
+                 void *stream);
+
+/*
  * Backward pass for callers that cannot allocate device memory.
  *
  * No counterpart on the pages: this is a library convenience.  Some callers are not
@@ -299,6 +339,16 @@ int fa_decode(const void *q, const void *k, const void *v, void *o, float *lse,
               const int *seqlens_k, void *workspace, size_t workspace_bytes, int B, int Hq,
               int Hkv, int Nq, int Nk, int d, int causal, int num_splits, float scale,
               void *stream);
+
+/*
+ * fa_decode with changed scores (softcap and alibi_slopes as for fa_fwd_score; the distance of
+ * new row t and key j is |seqlens_k[b] - Nq + t - j|).  num_splits and workspace as for
+ * fa_decode.  Rows of the cache behind the last valid key may hold anything.
+ */
+int fa_decode_score(const void *q, const void *k, const void *v, void *o, float *lse,
+                    const int *seqlens_k, const float *alibi_slopes, void *workspace,
+                    size_t workspace_bytes, int B, int Hq, int Hkv, int Nq, int Nk, int d,
+                    int causal, int num_splits, float softcap, float scale, void *stream);
 
 /*
  * The library's split count for fa_decode: enough (b, K/V head, key range) units to fill
