@@ -201,6 +201,11 @@ bool device_ready() {
     ok = ok && set_smem(fa::fa_decode_kernel<256, 16, true>, fa::DecodeLayout<256, 16>::kSmemBytes);
     ok = ok && set_smem(fa::fa_decode_kernel<256, 32, true>, fa::DecodeLayout<256, 32>::kSmemBytes);
     ok = ok && set_smem(fa::fa_decode_kernel<256, 64, true>, fa::DecodeLayout<256, 64>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kv4_kernel<64, 1>, fa::KV4Layout<64, 1>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kv4_kernel<64, 2>, fa::KV4Layout<64, 2>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kv4_kernel<128, 1>, fa::KV4Layout<128, 1>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kv4_kernel<128, 2>, fa::KV4Layout<128, 2>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kv4_kernel<256, 1>, fa::KV4Layout<256, 1>::kSmemBytes);
     using fa::FwdPLayout;
     ok = ok && set_smem(fa::fa_fwd_persist_kernel<64, fa::kAttnFull>, FwdPLayout<64>::kSmemBytes);
     ok = ok && set_smem(fa::fa_fwd_persist_kernel<64, fa::kAttnCausal>, FwdPLayout<64>::kSmemBytes);
@@ -431,14 +436,12 @@ int check_kv4_decode(int B, int Hq, int Hkv, int Nq, int cap, int d, float scale
   int rc = check_kv4_sizes(B, Hkv, cap, d);
   if (rc != FA_OK) return rc;
   if (Hq % Hkv != 0) return FA_ERR_GQA;
-  // grid.y holds (batch, K/V head)
-  if (static_cast<long long>(Hq / Hkv) * Nq > 128 || static_cast<long long>(B) * Hkv > 65535 ||
-      static_cast<long long>(B) * Hq * Nq >= (1ll << 31))
+  if (static_cast<long long>(Hq / Hkv) * Nq > 128 || static_cast<long long>(B) * Hq * Nq >= (1ll << 31))
     return FA_ERR_UNSUPPORTED;
   return FA_OK;
 }
 
-// 8-row tiles of query rows that one CTA takes.
+// 8-row tiles of query rows that one CTA takes together.
 int kv4_row_tiles(int R, int d) { return R > 8 && d != 256 ? 2 : 1; }
 
 // Writes (store) or reads n tokens of the cache.
@@ -459,11 +462,14 @@ int run_kv4_copy(bool store, fa::KV4Params &p, int d, cudaStream_t s) {
   return cuda_ok(cudaGetLastError(), store ? "fa_kv4_write launch" : "fa_kv4_read launch") ? FA_OK : FA_ERR_CUDA;
 }
 
+size_t kv4_workspace(int R, int d, int pieces) {
+  return pieces > 1 ? fa::pad256(static_cast<size_t>(pieces) * 2 * 8 * kv4_row_tiles(R, d) * (d + 2) * 4) : 0;
+}
+
 template <int D, int NT>
 void launch_kv4(const fa::KV4DecodeParams &p, cudaStream_t s) {
-  const dim3 grid(static_cast<unsigned>(p.splits), static_cast<unsigned>(p.B) * p.Hkv,
-                  static_cast<unsigned>((p.R + 8 * NT - 1) / (8 * NT)));
-  fa::fa_decode_kv4_kernel<D, NT><<<grid, fa::kKV4Warps * 32, 0, s>>>(p);
+  fa::fa_decode_kv4_kernel<D, NT>
+      <<<static_cast<unsigned>(p.pieces), fa::kKV4Warps * 32, fa::KV4Layout<D, NT>::kSmemBytes, s>>>(p);
 }
 
 // Launches the forward kernel for d (maps and parameters prepared by the caller).
@@ -1233,19 +1239,20 @@ int fa_decode_kv4_num_splits(int B, int Hq, int Hkv, int Nq, int cap, int d) {
     (void)cudaGetLastError();
     sms = 148;
   }
-  const int R = Hq / Hkv * Nq, rows = 8 * kv4_row_tiles(R, d);
-  const long long units = static_cast<long long>(B) * Hkv * ((R + rows - 1) / rows);
-  long long s = units >= 2 * sms ? 1 : 2 * sms / units;
-  const long long most = (cap + fa::kKV4Warps * fa::kKV4Keys - 1) / (fa::kKV4Warps * fa::kKV4Keys);
-  if (s > most) s = most;
-  if (s > kMaxDecodeSplits) s = kMaxDecodeSplits;
-  return static_cast<int>(s < 1 ? 1 : s);
+  // One piece per CTA that fits on the device at once (two CTAs an SM up to 8 rows and d = 128),
+  // but no more than there are blocks of 256 keys.
+  const int R = Hq / Hkv * Nq, tiles = kv4_row_tiles(R, d), rows = 8 * tiles;
+  const long long slots = static_cast<long long>(sms) * (tiles == 1 && d <= 128 ? 2 : 1);
+  const long long blocks = static_cast<long long>(B) * Hkv * ((R + rows - 1) / rows) *
+                           ((cap + fa::kKV4Block - 1) / fa::kKV4Block);
+  const long long s = blocks < slots ? blocks : slots;
+  return static_cast<int>(s < kMaxDecodeSplits ? s : kMaxDecodeSplits);
 }
 
 size_t fa_decode_kv4_workspace_bytes(int B, int Hq, int Hkv, int Nq, int cap, int d, int num_splits) {
   if (check_kv4_decode(B, Hq, Hkv, Nq, cap, d, 1.0f) != FA_OK) return 0;
   if (num_splits < 1 || num_splits > kMaxDecodeSplits) return 0;
-  return decode_workspace(B, Hq, Nq, d, num_splits);
+  return kv4_workspace(Hq / Hkv * Nq, d, num_splits);
 }
 
 int fa_decode_kv4(const void *q, const void *k_codes, const void *k_params, const void *v_codes, const void *v_params,
@@ -1258,7 +1265,7 @@ int fa_decode_kv4(const void *q, const void *k_codes, const void *k_params, cons
   int rc = check_kv4_decode(B, Hq, Hkv, Nq, cap, d, scale);
   if (rc == FA_OK) rc = check_score_args(softcap, alibi_slopes);
   if (rc != FA_OK) return rc;
-  const size_t need = decode_workspace(B, Hq, Nq, d, num_splits);
+  const size_t need = kv4_workspace(Hq / Hkv * Nq, d, num_splits);
   if (need > 0 && (!workspace || workspace_bytes < need)) return FA_ERR_WORKSPACE;
   const void *ptrs[] = {q, k_codes, k_params, v_codes, v_params, o, lse};
   for (const void *ptr : ptrs)
@@ -1277,31 +1284,32 @@ int fa_decode_kv4(const void *q, const void *k_codes, const void *k_params, cons
   p.slopes = alibi_slopes;
   p.o = static_cast<__nv_bfloat16 *>(o);
   p.lse = lse;
-  if (num_splits > 1) {
-    p.o_part = static_cast<float *>(workspace);
-    p.lse_part = reinterpret_cast<float *>(static_cast<char *>(workspace) +
-                                           fa::pad256(static_cast<size_t>(num_splits) * rows * d * 4));
-  }
+  p.part = static_cast<float *>(workspace);
   p.B = B;
   p.Hkv = Hkv;
   p.Nq = Nq;
   p.R = Hq / Hkv * Nq;
   p.cap = cap;
-  p.splits = num_splits;
-  const int per = (cap + num_splits - 1) / num_splits;
-  p.chunk = (per + fa::kKV4CapMultiple - 1) / fa::kKV4CapMultiple * fa::kKV4CapMultiple;
+  const bool two = kv4_row_tiles(p.R, d) == 2;
+  const int tile_rows = two ? 16 : 8;
+  p.row_tiles = (p.R + tile_rows - 1) / tile_rows;
+  p.pieces = num_splits;
   p.causal = causal;
   p.scale = scale;
   p.sl2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   p.softcap = softcap;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int tslot = timer_start(2, s);
-  const bool two = kv4_row_tiles(p.R, d) == 2;
   if (d == 64) two ? launch_kv4<64, 2>(p, s) : launch_kv4<64, 1>(p, s);
   else if (d == 128) two ? launch_kv4<128, 2>(p, s) : launch_kv4<128, 1>(p, s);
   else launch_kv4<256, 1>(p, s);
   timer_stop(2, tslot, s);
-  if (num_splits > 1) launch_merge(p.o_part, p.lse_part, o, lse, num_splits, static_cast<long long>(rows), d, s);
+  if (num_splits > 1 && cap > fa::kKV4Block) {  // segments of one block are never shared
+    const unsigned grid = static_cast<unsigned>((rows + 7) / 8);
+    if (d == 64) fa::fa_kv4_merge_kernel<64><<<grid, 256, 0, s>>>(p, tile_rows);
+    else if (d == 128) fa::fa_kv4_merge_kernel<128><<<grid, 256, 0, s>>>(p, tile_rows);
+    else fa::fa_kv4_merge_kernel<256><<<grid, 256, 0, s>>>(p, tile_rows);
+  }
   return cuda_ok(cudaGetLastError(), "fa_decode_kv4 launch") ? FA_OK : FA_ERR_CUDA;
 }
 

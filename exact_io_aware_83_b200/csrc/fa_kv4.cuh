@@ -26,6 +26,8 @@
 #include <cuda_fp16.h>
 
 #include "fa_common.cuh"
+#include "fa_fwd.cuh"
+#include "fa_score.cuh"
 
 namespace fa {
 
@@ -211,25 +213,55 @@ __global__ void __launch_bounds__(256) fa_kv4_read_kernel(const KV4Params p) {
 //    take without writing the widened values out and reading them back: 4 bytes a value
 //    through shared memory against half a byte from HBM.
 //  * Bound: HBM, 5 d / 4 bytes per key (K and V with their params).
+//  * Work: the valid tokens of every (batch entry, K/V head, row tile) - a segment - are cut
+//    into blocks of 256 keys, the blocks of all segments laid end to end and the line cut
+//    into `pieces` equal ranges, one CTA each, so that lengths that differ leave no SM idle.
+//    A segment that lies inside one piece is written by its CTA; one that several pieces
+//    share leaves a partial result per piece in the workspace, which fa_kv4_merge_kernel joins.
+//  * Each warp takes 32 keys of a block and streams its own tiles, across segments, through a
+//    ring of shared-memory stages filled by bulk copies (the rows of one head are contiguous);
+//    warps meet only where a segment ends.
 struct KV4DecodeParams {
   const __nv_bfloat16 *q;  // [B, Hq, Nq, D]
   const uint8_t *kc, *vc;
   const __half *kp, *vp;
   const int *lens;         // [B] (nullptr: all `cap`), clamped to [0, cap]
   const float *slopes;     // [Hq] or nullptr
-  __nv_bfloat16 *o;        // splits == 1
+  __nv_bfloat16 *o;
   float *lse;
-  float *o_part;           // [splits, B * Hq * Nq, D] fp32 (splits > 1)
-  float *lse_part;
+  float *part;             // [pieces][2][rows of a tile][D + 2] fp32 (O, then m and l)
   int B, Hkv, Nq, R, cap;
-  int splits, chunk;       // split s covers keys [s * chunk, (s + 1) * chunk)
+  int row_tiles, pieces;
   int causal;
   float scale, sl2;        // scale, scale * log2(e)
   float softcap;           // 0: none
 };
 
 constexpr int kKV4Warps = 8;
-constexpr int kKV4Keys = 32;  // keys per warp and iteration
+constexpr int kKV4Keys = 32;                        // keys per warp and step
+constexpr int kKV4Block = kKV4Warps * kKV4Keys;     // keys per block
+
+__device__ __forceinline__ int kv4_len(const KV4DecodeParams &p, int b) {
+  const int len = p.lens ? p.lens[b] : p.cap;
+  return len < 0 ? 0 : (len > p.cap ? p.cap : len);
+}
+// Blocks of a segment: one at least, so that a segment without keys is written too.
+__device__ __forceinline__ int kv4_blocks(int len) { return len > 0 ? (len + kKV4Block - 1) / kKV4Block : 1; }
+
+// Sum over the batch entries before `upto` of their blocks, times segments per entry (whole warp).
+__device__ __forceinline__ long long kv4_blocks_before(const KV4DecodeParams &p, int upto, int lane) {
+  long long n = 0;
+  for (int b = lane; b < upto; b += 32) n += kv4_blocks(kv4_len(p, b));
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
+  return n * (static_cast<long long>(p.Hkv) * p.row_tiles);
+}
+
+// First block of piece i of P over T blocks, and the piece that holds block x.
+__device__ __forceinline__ long long kv4_piece_begin(long long T, int P, int i) { return T * i / P; }
+__device__ __forceinline__ int kv4_piece_of(long long T, int P, long long x) {
+  return static_cast<int>(((x + 1) * P - 1) / T);
+}
 
 // The score in log2 units from x = scale q . k: capped, y = cap tanh(x / cap) log2(e).
 // tanh(u) = sign(u) (1 - w) / (1 + w), w = exp(-2 |u|): no cancellation that matters, the
@@ -273,320 +305,572 @@ __device__ __forceinline__ __half2 codes_h2(uint32_t w) {
   return __hsub2(u32_h2((w & mask) | magic), u32_h2(magic));
 }
 
-template <int D>
+template <int D, int NT>
 struct KV4Layout {
   static constexpr int G = D / 32;    // groups
   static constexpr int KW = G;        // K words per lane and key
   static constexpr int VW = D / 64;   // V words per lane and key
   static constexpr int MT = VW * 4;   // 16-channel tiles of O^T
+  static constexpr int ROWS = 8 * NT;
+  static constexpr int kCtas = NT == 1 && D <= 128 ? 2 : 1;  // CTAs per SM
+  // One stage of a warp's ring: codes and params of 32 keys.
+  static constexpr int kOffKC = 0;
+  static constexpr int kOffVC = kOffKC + kKV4Keys * D / 2;
+  static constexpr int kOffKP = kOffVC + kKV4Keys * D / 2;
+  static constexpr int kOffVP = kOffKP + kKV4Keys * 4 * G;
+  static constexpr int kStageBytes = kOffVP + kKV4Keys * 4 * G;
+  static constexpr int kPartBytes = kKV4Warps / 2 * ROWS * D * 4;  // O of half the warps, where a segment ends
+  static constexpr int kFixed = kPartBytes + 2 * kKV4Warps * ROWS * 4 + kKV4Warps * 8 * 8 + 64 + 128;
+  static constexpr int kFit = ((kCtas == 2 ? 232448 / 2 - 1024 : 232448) - kFixed) / (kKV4Warps * kStageBytes);
+  static constexpr int kStages = kFit > 4 ? 4 : kFit;
+  static constexpr int kOffPart = kKV4Warps * kStages * kStageBytes;
+  static constexpr int kOffM = kOffPart + kPartBytes;      // [warp][row] m, then l
+  static constexpr int kOffBar = kOffM + 2 * kKV4Warps * ROWS * 4;
+  static constexpr int kOffMisc = kOffBar + kKV4Warps * 8 * 8;
+  static constexpr int kSmemBytes = kOffMisc + 64 + 128;   // + slack for 128-byte alignment
+  static_assert(kStages >= 2 && kStages <= 8, "ring");
 };
 
 // Key of row r of a 16-key step: the rows 2c, 2c+1, 2c+8, 2c+9 of lane group c of the second
-// product are the keys c, c+4, c+8, c+12, so that its four loads cover consecutive tokens.
+// product are the keys c, c+4, c+8, c+12, so that its four loads touch consecutive tokens
+// and no two lanes of a load the same bank.
 __device__ __forceinline__ int kv4_key_of_row(int r) { return ((r & 7) >> 1) + 4 * (r & 1) + (r & 8); }
 
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_t bytes, uint32_t bar) {
+  asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+               "l"(src), "r"(bytes), "r"(bar)
+               : "memory");
+}
+
+// A block of the line: its segment and its place in it.
+struct KV4Cursor {
+  int b, seg, blk, nblk, len;  // seg: kvh * row_tiles + row tile
+  __device__ __forceinline__ void enter(const KV4DecodeParams &p, int b_) {
+    b = b_;
+    len = kv4_len(p, b);
+    nblk = kv4_blocks(len);
+  }
+  __device__ __forceinline__ void next(const KV4DecodeParams &p) {
+    if (++blk < nblk) return;
+    blk = 0;
+    if (++seg < p.Hkv * p.row_tiles) return;
+    seg = 0;
+    if (b + 1 < p.B) enter(p, b + 1);
+  }
+};
+
 template <int D, int NT>
-__global__ void __launch_bounds__(kKV4Warps * 32) fa_decode_kv4_kernel(const KV4DecodeParams p) {
-  using L = KV4Layout<D>;
-  constexpr int G = L::G, KW = L::KW, VW = L::VW, MT = L::MT;
-  constexpr int ROWS = 8 * NT;
-  __shared__ float sm_o[kKV4Warps][ROWS][D / 8];  // combined in 8 passes over the channels
-  __shared__ float sm_m[kKV4Warps][ROWS], sm_l[kKV4Warps][ROWS];
+__global__ void __launch_bounds__(kKV4Warps * 32, KV4Layout<D, NT>::kCtas)
+    fa_decode_kv4_kernel(const KV4DecodeParams p) {
+  using L = KV4Layout<D, NT>;
+  constexpr int G = L::G, KW = L::KW, VW = L::VW, MT = L::MT, S = L::kStages, ROWS = L::ROWS;
+  extern __shared__ uint8_t smem_raw[];
+  const uint32_t base = (smem_u32(smem_raw) + 127u) & ~127u;
+  uint8_t *smem = smem_raw + (base - smem_u32(smem_raw));
+  float *sm_o = reinterpret_cast<float *>(smem + L::kOffPart);
+  float *sm_m = reinterpret_cast<float *>(smem + L::kOffM), *sm_l = sm_m + kKV4Warps * ROWS;
+  int *misc = reinterpret_cast<int *>(smem + L::kOffMisc);  // [0] abort flag, [2..] line
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane / 4, c = lane % 4;
-  const int split = blockIdx.x, bh = blockIdx.y, r0 = blockIdx.z * ROWS;
-  const int b = bh / p.Hkv, kvh = bh % p.Hkv;
-  const int grp = p.R / p.Nq;  // query heads per K/V head
-  int len = p.lens ? p.lens[b] : p.cap;
-  len = len < 0 ? 0 : (len > p.cap ? p.cap : len);
-  const int k_begin = split * p.chunk;
-  const int k_end = min(k_begin + p.chunk, len);
-  const long long rows_total = static_cast<long long>(p.B) * p.Hkv * p.R;
-  const long long row0 = static_cast<long long>(bh) * p.R + r0;
-  const int pos0 = len - p.Nq;
+  const uint32_t ring = base + warp * (S * L::kStageBytes);
+  uint8_t *ring_ptr = smem + warp * (S * L::kStageBytes);
+  const uint32_t bars = base + L::kOffBar + warp * 64;
+  volatile int *abort_flag = misc;
 
-  // ---- Q fragments: row g of each 8-row tile, this lane's 8 channels of every group, scaled
-  uint32_t qf[NT][G][4];         // [2 t + e]: channels (2t + e, 2t + e + 4) of the word
-  float fac[NT][2];              // rows 2c, 2c+1: scale (or scale log2 e without a cap) / row scaling
-  float qsum[NT][G][2];          // rows 2c, 2c+1: sum of the scaled q over each group
-  float slope2[NT][2];
-  int rpos[NT][2];               // position of the row
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    const int r = nt * 8 + g;
-    const bool rv = r0 + r < p.R;
-    float x[G][8];
-    float amax = 0.f;
-#pragma unroll
-    for (int i = 0; i < G; ++i) {
-      uint4 w = make_uint4(0, 0, 0, 0);
-      if (rv) w = *reinterpret_cast<const uint4 *>(p.q + (row0 + r) * D + 32 * i + 8 * c);
-      unpack_bf16x8(w, x[i]);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[i][e]));
+  // ---- this piece of the line: blocks [x0, x1), and the segment that x0 lies in
+  if (lane < S) mbar_init(bars + 8 * lane, 1);
+  fence_mbar_init();
+  if (warp == 0) {
+    const long long per = static_cast<long long>(p.Hkv) * p.row_tiles;
+    long long T;
+    if (!p.lens) {
+      T = static_cast<long long>(p.B) * per * kv4_blocks(p.cap);
+    } else {
+      T = kv4_blocks_before(p, p.B, lane);
     }
+    const long long x0 = kv4_piece_begin(T, p.pieces, blockIdx.x), x1 = kv4_piece_begin(T, p.pieces, blockIdx.x + 1);
+    // the batch entry that holds block x0: 32 entries at a time
+    long long before = 0;
+    int b = 0;
+    for (int b0 = 0; b0 < p.B; b0 += 32) {
+      const long long n = b0 + lane < p.B ? kv4_blocks(kv4_len(p, b0 + lane)) * per : 0;
+      long long sum = n;
 #pragma unroll
-    for (int o = 1; o < 4; o *= 2) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    // largest magnitude into [128, 256)
-    const int ex = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100);
-    const float up = __uint_as_float(static_cast<uint32_t>(127 + 7 - ex) << 23);
-    const float down = __uint_as_float(static_cast<uint32_t>(127 - 7 + ex) << 23);
-#pragma unroll
-    for (int i = 0; i < G; ++i) {
-      float s = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        x[i][e] *= up;
-        s += x[i][e];
+      for (int o = 1; o < 32; o *= 2) {
+        const long long t = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o) sum += t;
       }
-#pragma unroll
-      for (int e = 0; e < 4; ++e) qf[nt][i][e] = pack_f16x2(x[i][e], x[i][e + 4]);
-#pragma unroll
-      for (int o = 1; o < 4; o *= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
-      qsum[nt][i][0] = __shfl_sync(0xffffffffu, s, 8 * c);
-      qsum[nt][i][1] = __shfl_sync(0xffffffffu, s, 8 * c + 4);
+      const uint32_t hit = __ballot_sync(0xffffffffu, before + sum > x0 && n > 0);
+      if (hit) {
+        const int l = __ffs(hit) - 1;
+        b = b0 + l;
+        before += __shfl_sync(0xffffffffu, sum - n, l);
+        break;
+      }
+      before += __shfl_sync(0xffffffffu, sum, 31);
     }
-    const float f = (p.softcap > 0.f ? p.scale : p.sl2) * down;
-    fac[nt][0] = __shfl_sync(0xffffffffu, f, 8 * c);
-    fac[nt][1] = __shfl_sync(0xffffffffu, f, 8 * c + 4);
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int rr = r0 + nt * 8 + 2 * c + e;
-      const int h = kvh * grp + min(rr / p.Nq, grp - 1);
-      slope2[nt][e] = p.slopes ? p.slopes[h] * 1.4426950408889634f : 0.f;
-      rpos[nt][e] = pos0 + rr % p.Nq;
+    if (lane == 0) {
+      const int nblk = kv4_blocks(kv4_len(p, b));
+      const long long in = x0 - before;
+      misc[0] = 0;
+      misc[2] = static_cast<int>(x1 - x0);
+      misc[3] = b;
+      misc[4] = static_cast<int>(in / nblk);
+      misc[5] = static_cast<int>(in % nblk);
     }
   }
-  const float inv_cap2 = p.softcap > 0.f ? 2.f * 1.4426950408889634f / p.softcap : 0.f;
-  const float cap_log2 = p.softcap * 1.4426950408889634f;
+  __syncthreads();
+  int todo = misc[2];  // blocks left
+  KV4Cursor cur;       // what is computed next
+  cur.enter(p, misc[3]);
+  cur.seg = misc[4];
+  cur.blk = misc[5];
+  KV4Cursor ahead = cur;  // what is loaded next
+  int ahead_todo = todo, issued = 0, taken = 0;
+  bool ok = true;
 
-  float acc[MT][NT][4];
-#pragma unroll
-  for (int i = 0; i < MT; ++i)
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) acc[i][nt][e] = 0.f;
-  float m_run[NT][2], l_run[NT][2];
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt) {
-    m_run[nt][0] = m_run[nt][1] = -INFINITY;
-    l_run[nt][0] = l_run[nt][1] = 0.f;
-  }
+  // Starts the copies of this warp's next tile that has keys, if any is left.
+  auto issue = [&]() {
+    while (ahead_todo > 0) {
+      const int kb = ahead.blk * kKV4Block + warp * kKV4Keys;
+      const bool has = kb < ahead.len;
+      if (has && lane == 0) {
+        const int st = issued % S;
+        const uint32_t dst = ring + st * L::kStageBytes, bar = bars + 8 * st;
+        const long long row = static_cast<long long>(ahead.b * p.Hkv + ahead.seg / p.row_tiles) * p.cap + kb;
+        mbar_arrive_expect_tx(bar, L::kStageBytes);
+        bulk_load(dst + L::kOffKC, p.kc + row * (D / 2), kKV4Keys * D / 2, bar);
+        bulk_load(dst + L::kOffVC, p.vc + row * (D / 2), kKV4Keys * D / 2, bar);
+        bulk_load(dst + L::kOffKP, p.kp + row * (2 * G), kKV4Keys * 4 * G, bar);
+        bulk_load(dst + L::kOffVP, p.vp + row * (2 * G), kKV4Keys * 4 * G, bar);
+      }
+      ahead.next(p);
+      --ahead_todo;
+      if (has) {
+        ++issued;
+        return;
+      }
+    }
+  };
+#pragma unroll 1
+  for (int i = 0; i < S; ++i) issue();
 
-  const long long crow0 = static_cast<long long>(bh) * p.cap;
+  const int grp = p.R / p.Nq;  // query heads per K/V head
+  const float inv_cap2 = p.softcap > 0.f ? 2.f * kLog2e / p.softcap : 0.f;
+  const float cap_log2 = p.softcap * kLog2e;
   const int ka = kv4_key_of_row(g);  // key of row g; row g + 8 is ka + 8
   const int vgroup = (g * VW) / 4;   // group of this lane's V channels
 
-  for (int kb = k_begin + warp * kKV4Keys; kb < k_end; kb += kKV4Warps * kKV4Keys) {
-    float y[2][NT][4];  // [step][tile][key A: rows 2c, 2c+1; key B: rows 2c, 2c+1]
+  while (todo > 0) {
+    // ---- one segment, or the part of it that lies in this piece
+    const int blk0 = cur.blk, count = min(cur.nblk - blk0, todo), len = cur.len;
+    const bool began_before = blk0 > 0, ends_after = blk0 + count < cur.nblk;
+    const int kvh = cur.seg / p.row_tiles, r0 = (cur.seg % p.row_tiles) * ROWS;
+    const long long row0 = static_cast<long long>(cur.b * p.Hkv + kvh) * p.R + r0;
+    const int pos0 = len - p.Nq;
+
+    // Q fragments: row g of each 8-row tile, this lane's 8 channels of every group, scaled
+    uint32_t qf[NT][G][4];         // [e]: channels (e, e + 4) of the word
+    float fac[NT][2];              // rows 2c, 2c+1: scale (or scale log2 e without a cap) / row scaling
+    float qsum[NT][G][2];          // rows 2c, 2c+1: sum of the scaled q over each group
+    float slope2[NT][2];
+    int rpos[NT][2];               // position of the row
 #pragma unroll
-    for (int st = 0; st < 2; ++st) {
-      const int key0 = kb + 16 * st;
-      const long long krow = crow0 + key0 + ka;
-      uint32_t w[2][KW];
-      __half sc[2][G], mn[2][G];
+    for (int nt = 0; nt < NT; ++nt) {
+      const int r = nt * 8 + g;
+      const bool rv = r0 + r < p.R;
+      float x[G][8];
+      float amax = 0.f;
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (rv) w = *reinterpret_cast<const uint4 *>(p.q + (row0 + r) * D + 32 * i + 8 * c);
+        unpack_bf16x8(w, x[i]);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[i][e]));
+      }
+#pragma unroll
+      for (int o = 1; o < 4; o *= 2) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
+      // largest magnitude into [128, 256)
+      const int ex = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100);
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + 7 - ex) << 23);
+      const float down = __uint_as_float(static_cast<uint32_t>(127 - 7 + ex) << 23);
+#pragma unroll
+      for (int i = 0; i < G; ++i) {
+        float s = 0.f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          x[i][e] *= up;
+          s += x[i][e];
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) qf[nt][i][e] = pack_f16x2(x[i][e], x[i][e + 4]);
+#pragma unroll
+        for (int o = 1; o < 4; o *= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+        qsum[nt][i][0] = __shfl_sync(0xffffffffu, s, 8 * c);
+        qsum[nt][i][1] = __shfl_sync(0xffffffffu, s, 8 * c + 4);
+      }
+      const float f = (p.softcap > 0.f ? p.scale : p.sl2) * down;
+      fac[nt][0] = __shfl_sync(0xffffffffu, f, 8 * c);
+      fac[nt][1] = __shfl_sync(0xffffffffu, f, 8 * c + 4);
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        const uint32_t *src = reinterpret_cast<const uint32_t *>(p.kc + (krow + 8 * e) * (D / 2)) + c * KW;
-        if constexpr (KW == 2) {
-          *reinterpret_cast<uint2 *>(w[e]) = *reinterpret_cast<const uint2 *>(src);
-        } else {
-#pragma unroll
-          for (int i = 0; i < KW; i += 4) *reinterpret_cast<uint4 *>(w[e] + i) = *reinterpret_cast<const uint4 *>(src + i);
-        }
-        const __half *par = p.kp + (krow + 8 * e) * (2 * G);
-#pragma unroll
-        for (int i = 0; i < G; ++i) {
-          sc[e][i] = par[i];
-          mn[e][i] = par[G + i];
-        }
+        const int rr = r0 + nt * 8 + 2 * c + e;
+        const int h = kvh * grp + min(rr / p.Nq, grp - 1);
+        slope2[nt][e] = p.slopes ? p.slopes[h] * kLog2e : 0.f;
+        rpos[nt][e] = pos0 + rr % p.Nq;
       }
+    }
+
+    float acc[MT][NT][4];
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[st][nt][e] = 0.f;
+        for (int e = 0; e < 4; ++e) acc[i][nt][e] = 0.f;
+    float m_run[NT][2], l_run[NT][2];
 #pragma unroll
-      for (int i = 0; i < G; ++i) {
-        float part[NT][4];
+    for (int nt = 0; nt < NT; ++nt) {
+      m_run[nt][0] = m_run[nt][1] = -INFINITY;
+      l_run[nt][0] = l_run[nt][1] = 0.f;
+    }
+
+#pragma unroll 1
+    for (int blk = blk0; blk < blk0 + count; ++blk) {
+      const int kb = blk * kKV4Block + warp * kKV4Keys;
+      if (kb >= len) continue;
+      const int st_ = taken % S;
+      if (ok) ok = warp_wait_bounded(bars + 8 * st_, (taken / S) & 1, abort_flag, wait_site(5, st_, taken));
+      if (!ok) continue;  // the flag is up: nothing of this call is valid any more
+      ++taken;
+      const uint8_t *stage = ring_ptr + st_ * L::kStageBytes;
+      float y[2][NT][4];  // [step][tile][key A: rows 2c, 2c+1; key B: rows 2c, 2c+1]
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        uint32_t w[2][KW];
+        uint32_t par[2][G];  // s of the groups in pairs, then m in pairs
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int key = 16 * st + ka + 8 * e;
+          const uint32_t *src = reinterpret_cast<const uint32_t *>(stage + L::kOffKC + key * (D / 2)) + c * KW;
+          const uint32_t *ps = reinterpret_cast<const uint32_t *>(stage + L::kOffKP + key * (4 * G));
+          if constexpr (KW == 2) {
+            *reinterpret_cast<uint2 *>(w[e]) = *reinterpret_cast<const uint2 *>(src);
+            *reinterpret_cast<uint2 *>(par[e]) = *reinterpret_cast<const uint2 *>(ps);
+          } else {
+#pragma unroll
+            for (int i = 0; i < KW; i += 4) {
+              *reinterpret_cast<uint4 *>(w[e] + i) = *reinterpret_cast<const uint4 *>(src + i);
+              *reinterpret_cast<uint4 *>(par[e] + i) = *reinterpret_cast<const uint4 *>(ps + i);
+            }
+          }
+        }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) part[nt][e] = 0.f;
-        uint32_t a[2][4];
+          for (int e = 0; e < 4; ++e) y[st][nt][e] = 0.f;
 #pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          a[e][0] = h2_u32(codes_h2<0>(w[e][i]));
-          a[e][1] = h2_u32(codes_h2<1>(w[e][i]));
-          a[e][2] = h2_u32(codes_h2<0>(w[e][i] >> 8));
-          a[e][3] = h2_u32(codes_h2<1>(w[e][i] >> 8));
+        for (int i = 0; i < G; ++i) {
+          float part[NT][4];
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) part[nt][e] = 0.f;
+          uint32_t a[2][4];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            a[e][0] = h2_u32(codes_h2<0>(w[e][i]));
+            a[e][1] = h2_u32(codes_h2<1>(w[e][i]));
+            a[e][2] = h2_u32(codes_h2<0>(w[e][i] >> 8));
+            a[e][3] = h2_u32(codes_h2<1>(w[e][i] >> 8));
+          }
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_f16_16816(part[nt], a[0][0], a[1][0], a[0][1], a[1][1], qf[nt][i][0], qf[nt][i][1]);
+            mma_f16_16816(part[nt], a[0][2], a[1][2], a[0][3], a[1][3], qf[nt][i][2], qf[nt][i][3]);
+          }
+          auto pick = [](uint32_t u, int hi) { return __half2float(hi ? __high2half(u32_h2(u)) : __low2half(u32_h2(u))); };
+          const float sA = pick(par[0][i / 2], i & 1), sB = pick(par[1][i / 2], i & 1);
+          const float mA = pick(par[0][G / 2 + i / 2], i & 1), mB = pick(par[1][G / 2 + i / 2], i & 1);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            y[st][nt][0] = fmaf(sA, part[nt][0], fmaf(mA, qsum[nt][i][0], y[st][nt][0]));
+            y[st][nt][1] = fmaf(sA, part[nt][1], fmaf(mA, qsum[nt][i][1], y[st][nt][1]));
+            y[st][nt][2] = fmaf(sB, part[nt][2], fmaf(mB, qsum[nt][i][0], y[st][nt][2]));
+            y[st][nt][3] = fmaf(sB, part[nt][3], fmaf(mB, qsum[nt][i][1], y[st][nt][3]));
+          }
         }
+        // ---- cap, bias, mask: the scores in log2 units
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma_f16_16816(part[nt], a[0][0], a[1][0], a[0][1], a[1][1], qf[nt][i][0], qf[nt][i][1]);
-          mma_f16_16816(part[nt], a[0][2], a[1][2], a[0][3], a[1][3], qf[nt][i][2], qf[nt][i][3]);
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[st][nt][e] *= fac[nt][e & 1];
+        if (p.softcap > 0.f) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) y[st][nt][e] = softcap_log2(y[st][nt][e], inv_cap2, cap_log2);
         }
-        const float sA = __half2float(sc[0][i]), sB = __half2float(sc[1][i]);
-        const float mA = __half2float(mn[0][i]), mB = __half2float(mn[1][i]);
+        if (p.slopes) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          y[st][nt][0] = fmaf(sA, part[nt][0], fmaf(mA, qsum[nt][i][0], y[st][nt][0]));
-          y[st][nt][1] = fmaf(sA, part[nt][1], fmaf(mA, qsum[nt][i][1], y[st][nt][1]));
-          y[st][nt][2] = fmaf(sB, part[nt][2], fmaf(mB, qsum[nt][i][0], y[st][nt][2]));
-          y[st][nt][3] = fmaf(sB, part[nt][3], fmaf(mB, qsum[nt][i][1], y[st][nt][3]));
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = kb + 16 * st + ka + 8 * (e / 2);
+              y[st][nt][e] = fmaf(-slope2[nt][e & 1], fabsf(static_cast<float>(rpos[nt][e & 1] - key)), y[st][nt][e]);
+            }
         }
       }
-      // ---- cap, bias, mask: the scores in log2 units
+      if (kb + kKV4Keys > (p.causal ? min(len, pos0 + 1) : len)) {  // some key is hidden from some row
+#pragma unroll
+        for (int st = 0; st < 2; ++st)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = kb + 16 * st + ka + 8 * (e / 2);
+              if (key >= len || (p.causal && key > rpos[nt][e & 1])) y[st][nt][e] = -INFINITY;
+            }
+      }
+      // ---- running maximum: moved (for the whole warp) only when a row's rises by more than 2^8
+      bool up = false;
+      float mx[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const int key = key0 + ka + 8 * (e / 2);
-          float v = y[st][nt][e] * fac[nt][e & 1];
-          if (p.softcap > 0.f) v = softcap_log2(v, inv_cap2, cap_log2);
-          if (p.slopes) v = fmaf(-slope2[nt][e & 1], fabsf(static_cast<float>(rpos[nt][e & 1] - key)), v);
-          if (key >= k_end || (p.causal && key > rpos[nt][e & 1])) v = -INFINITY;
-          y[st][nt][e] = v;
+        for (int e = 0; e < 2; ++e) {
+          mx[nt][e] = fmaxf(fmaxf(y[0][nt][e], y[0][nt][e + 2]), fmaxf(y[1][nt][e], y[1][nt][e + 2]));
+          up |= mx[nt][e] > m_run[nt][e] + 8.f;
         }
+      if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float alpha[2];
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float v = mx[nt][e];
+#pragma unroll
+            for (int o = 4; o < 32; o *= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+            const float mn = fmaxf(m_run[nt][e], v);
+            alpha[e] = mn == m_run[nt][e] ? 1.f : ex2_approx(m_run[nt][e] - mn);  // 0 at the first keys
+            m_run[nt][e] = mn;
+            l_run[nt][e] *= alpha[e];
+          }
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[i][nt][e] *= alpha[e & 1];
+        }
+      }
+#pragma unroll
+      for (int st = 0; st < 2; ++st) {
+        uint32_t pb[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float pr[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const float mu = m_run[nt][e & 1] == -INFINITY ? 0.f : m_run[nt][e & 1];
+            pr[e] = ex2_approx(y[st][nt][e] - mu);
+            l_run[nt][e & 1] += pr[e];
+          }
+          pb[nt][0] = movmatrix_trans(pack_f16x2(pr[0], pr[1]));
+          pb[nt][1] = movmatrix_trans(pack_f16x2(pr[2], pr[3]));
+        }
+        uint32_t wv[4][VW], sm[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int key = 16 * st + c + 4 * e;
+          const uint32_t *src = reinterpret_cast<const uint32_t *>(stage + L::kOffVC + key * (D / 2)) + g * VW;
+          if constexpr (VW == 1) wv[e][0] = *src;
+          else if constexpr (VW == 2) *reinterpret_cast<uint2 *>(wv[e]) = *reinterpret_cast<const uint2 *>(src);
+          else *reinterpret_cast<uint4 *>(wv[e]) = *reinterpret_cast<const uint4 *>(src);
+          sm[e] = reinterpret_cast<const uint32_t *>(stage + L::kOffVP + key * (4 * G))[vgroup];
+        }
+        if (kb + kKV4Keys > len) {
+          // rows behind the last key hold anything; 0 * NaN would spread
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (kb + 16 * st + c + 4 * e >= len) sm[e] = 0u;
+        }
+        __half2 sp[2], mp[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          sp[e] = u32_h2(__byte_perm(sm[2 * e], sm[2 * e + 1], 0x5410));
+          mp[e] = u32_h2(__byte_perm(sm[2 * e], sm[2 * e + 1], 0x7632));
+        }
+#pragma unroll
+        for (int w = 0; w < VW; ++w)
+#pragma unroll
+          for (int half = 0; half < 2; ++half) {
+            uint32_t x[2];  // key pairs; the four codes of two bytes in each half
+#pragma unroll
+            for (int e = 0; e < 2; ++e) x[e] = __byte_perm(wv[2 * e][w], wv[2 * e + 1][w], half ? 0x7632 : 0x5410);
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+              const uint32_t x0 = t ? x[0] >> 8 : x[0], x1 = t ? x[1] >> 8 : x[1];
+              const uint32_t a0 = h2_u32(__hfma2(codes_h2<0>(x0), sp[0], mp[0]));
+              const uint32_t a1 = h2_u32(__hfma2(codes_h2<1>(x0), sp[0], mp[0]));
+              const uint32_t a2 = h2_u32(__hfma2(codes_h2<0>(x1), sp[1], mp[1]));
+              const uint32_t a3 = h2_u32(__hfma2(codes_h2<1>(x1), sp[1], mp[1]));
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+                mma_f16_16816(acc[w * 4 + half * 2 + t][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
+            }
+          }
+      }
+      __syncwarp();  // every lane has read the stage
+      issue();
     }
-    // ---- running maximum: moved (for the whole warp) only when a row's rises by more than 2^8
-    bool up = false;
-    float mx[NT][2];
+
+    // ---- the segment's end: join the warps (those without keys have m = -inf, l = 0, O = 0).
+    // Warps 4-7 hand their O, brought to the common maximum, to warps 0-3, which add their own;
+    // then every thread sums four of them.
+    __syncthreads();  // sm_* of the previous segment have been read
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        mx[nt][e] = fmaxf(fmaxf(y[0][nt][e], y[0][nt][e + 2]), fmaxf(y[1][nt][e], y[1][nt][e + 2]));
-        up |= mx[nt][e] > m_run[nt][e] + 8.f;
-      }
-    if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float alpha[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-          float v = mx[nt][e];
-#pragma unroll
-          for (int o = 4; o < 32; o *= 2) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
-          const float mn = fmaxf(m_run[nt][e], v);
-          alpha[e] = mn == m_run[nt][e] ? 1.f : ex2_approx(m_run[nt][e] - mn);  // 0 at the first keys
-          m_run[nt][e] = mn;
-          l_run[nt][e] *= alpha[e];
+        for (int o = 4; o < 32; o *= 2) l_run[nt][e] += __shfl_xor_sync(0xffffffffu, l_run[nt][e], o);
+        if (g == 0) {
+          sm_m[warp * ROWS + nt * 8 + 2 * c + e] = m_run[nt][e];
+          sm_l[warp * ROWS + nt * 8 + 2 * c + e] = l_run[nt][e];
         }
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) acc[i][nt][e] *= alpha[e & 1];
       }
-    }
+    __syncthreads();
+    float scale_w[NT][2];
 #pragma unroll
-    for (int st = 0; st < 2; ++st) {
-      uint32_t pb[NT][2];
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float pr[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float mu = m_run[nt][e & 1] == -INFINITY ? 0.f : m_run[nt][e & 1];
-          pr[e] = ex2_approx(y[st][nt][e] - mu);
-          l_run[nt][e & 1] += pr[e];
-        }
-        pb[nt][0] = movmatrix_trans(pack_f16x2(pr[0], pr[1]));
-        pb[nt][1] = movmatrix_trans(pack_f16x2(pr[2], pr[3]));
-      }
-      const int key0 = kb + 16 * st;
-      uint32_t wv[4][VW], sm[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int key = key0 + c + 4 * e;
-        const uint32_t *src = reinterpret_cast<const uint32_t *>(p.vc + (crow0 + key) * (D / 2)) + g * VW;
-        if constexpr (VW == 1) wv[e][0] = *src;
-        else if constexpr (VW == 2) *reinterpret_cast<uint2 *>(wv[e]) = *reinterpret_cast<const uint2 *>(src);
-        else *reinterpret_cast<uint4 *>(wv[e]) = *reinterpret_cast<const uint4 *>(src);
-        sm[e] = reinterpret_cast<const uint32_t *>(p.vp + (crow0 + key) * (2 * G))[vgroup];
-        if (key >= k_end) sm[e] = 0u;  // rows behind the last key hold anything; 0 * NaN would spread
-      }
-      __half2 sp[2], mp[2];
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        sp[e] = u32_h2(__byte_perm(sm[2 * e], sm[2 * e + 1], 0x5410));
-        mp[e] = u32_h2(__byte_perm(sm[2 * e], sm[2 * e + 1], 0x7632));
+        float m = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kKV4Warps; ++w) m = fmaxf(m, sm_m[w * ROWS + nt * 8 + 2 * c + e]);
+        scale_w[nt][e] = ex2_approx(m_run[nt][e] - (m == -INFINITY ? 0.f : m));
       }
 #pragma unroll
-      for (int w = 0; w < VW; ++w)
-#pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          uint32_t x[2];  // key pairs; the four codes of two bytes in each half
-#pragma unroll
-          for (int e = 0; e < 2; ++e) x[e] = __byte_perm(wv[2 * e][w], wv[2 * e + 1][w], half ? 0x7632 : 0x5410);
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            const uint32_t x0 = t ? x[0] >> 8 : x[0], x1 = t ? x[1] >> 8 : x[1];
-            const uint32_t a0 = h2_u32(__hfma2(codes_h2<0>(x0), sp[0], mp[0]));
-            const uint32_t a1 = h2_u32(__hfma2(codes_h2<1>(x0), sp[0], mp[0]));
-            const uint32_t a2 = h2_u32(__hfma2(codes_h2<0>(x1), sp[1], mp[1]));
-            const uint32_t a3 = h2_u32(__hfma2(codes_h2<1>(x1), sp[1], mp[1]));
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_f16_16816(acc[w * 4 + half * 2 + t][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
-          }
-        }
-    }
-  }
-
-  // ---- combine the warps: m, l of every row, then O an eighth of the channels at a time
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-#pragma unroll
-      for (int o = 4; o < 32; o *= 2) l_run[nt][e] += __shfl_xor_sync(0xffffffffu, l_run[nt][e], o);
-      if (g == 0) {
-        sm_m[warp][nt * 8 + 2 * c + e] = m_run[nt][e];
-        sm_l[warp][nt * 8 + 2 * c + e] = l_run[nt][e];
-      }
-    }
-  // Accumulator tile w * 4 + q of lane (g, c): channels 8 (g VW + w) + 2 q (+ 1), rows 2c, 2c+1.
-#pragma unroll 1
-  for (int pass = 0; pass < 8; ++pass) {
-    __syncthreads();
-    if (g == pass) {
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
+    for (int turn = 0; turn < 2; ++turn) {
+      if (warp / 4 == 1 - turn) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sm_o[warp][nt * 8 + 2 * c + (e & 1)][2 * i + e / 2] = acc[i][nt][e];
+          for (int e = 0; e < 2; ++e) {
+            const int r = nt * 8 + 2 * c + e;
+            if (r0 + r >= p.R) continue;
+            // Accumulator tile w * 4 + q of lane (g, c): channels 8 (g VW + w) + 2 q (+ 1), rows 2c, 2c+1.
+            float4 *dst = reinterpret_cast<float4 *>(sm_o + ((warp % 4) * ROWS + r) * D + 8 * g * VW);
+            const float f = scale_w[nt][e];
+#pragma unroll
+            for (int i = 0; i < MT; i += 2) {
+              float4 v = turn ? dst[i / 2] : make_float4(0.f, 0.f, 0.f, 0.f);
+              v.x = fmaf(f, acc[i][nt][e], v.x);
+              v.y = fmaf(f, acc[i][nt][e + 2], v.y);
+              v.z = fmaf(f, acc[i + 1][nt][e], v.z);
+              v.w = fmaf(f, acc[i + 1][nt][e + 2], v.w);
+              dst[i / 2] = v;
+            }
+          }
+      }
+      __syncthreads();
     }
-    __syncthreads();
-    for (int idx = threadIdx.x; idx < ROWS * (D / 8); idx += blockDim.x) {
-      const int r = idx / (D / 8), ch = idx % (D / 8);
-      if (r0 + r >= p.R) continue;
-      float m = -INFINITY;
+    if (*abort_flag == 0) {
+      const bool direct = !began_before && !ends_after;
+      float *part = p.part + (static_cast<long long>(blockIdx.x) * 2 + (began_before ? 0 : 1)) * (ROWS * (D + 2));
+      for (int idx = threadIdx.x; idx < ROWS * (D / 2); idx += blockDim.x) {
+        const int r = idx / (D / 2), ch = 2 * (idx % (D / 2));
+        if (r0 + r >= p.R) break;
+        float m = -INFINITY;
 #pragma unroll
-      for (int w = 0; w < kKV4Warps; ++w) m = fmaxf(m, sm_m[w][r]);
-      const float mu = m == -INFINITY ? 0.f : m;
-      float l = 0.f, o = 0.f;
+        for (int w = 0; w < kKV4Warps; ++w) m = fmaxf(m, sm_m[w * ROWS + r]);
+        const float mu = m == -INFINITY ? 0.f : m;
+        float l = 0.f, o0 = 0.f, o1 = 0.f;
 #pragma unroll
-      for (int w = 0; w < kKV4Warps; ++w) {
-        const float f = ex2_approx(sm_m[w][r] - mu);
-        l = fmaf(f, sm_l[w][r], l);
-        o = fmaf(f, sm_o[w][r][ch], o);
+        for (int w = 0; w < kKV4Warps; ++w) l = fmaf(ex2_approx(sm_m[w * ROWS + r] - mu), sm_l[w * ROWS + r], l);
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const float2 o = *reinterpret_cast<const float2 *>(sm_o + (w * ROWS + r) * D + ch);
+          o0 += o.x;
+          o1 += o.y;
+        }
+        if (direct) {
+          const float inv = l == 0.f ? 0.f : 1.f / l;  // a row without keys: 0; NaN stays NaN
+          *reinterpret_cast<uint32_t *>(p.o + (row0 + r) * D + ch) = pack_bf16x2(o0 * inv, o1 * inv);
+          if (ch == 0) p.lse[row0 + r] = l == 0.f ? -INFINITY : (mu + log2f(l)) * kLn2;
+        } else {
+          float *dst = part + r * (D + 2);
+          *reinterpret_cast<float2 *>(dst + ch) = make_float2(o0, o1);
+          if (ch == 0) {
+            dst[D] = m;
+            dst[D + 1] = l;
+          }
+        }
       }
-      o = l == 0.f ? 0.f : o / l;  // a row without keys: 0; NaN stays NaN
-      const float lse = l == 0.f ? -INFINITY : (mu + log2f(l)) * kLn2;
-      const long long row = row0 + r;
-      if (p.splits == 1) {
-        p.o[row * D + pass * (D / 8) + ch] = __float2bfloat16_rn(o);
-        if (pass == 0 && ch == 0) p.lse[row] = lse;
-      } else {
-        const long long prow = static_cast<long long>(split) * rows_total + row;
-        p.o_part[prow * D + pass * (D / 8) + ch] = o;
-        if (pass == 0 && ch == 0) p.lse_part[prow] = lse;
-      }
+    }
+    todo -= count;
+    cur.blk = cur.nblk - 1;  // to the next segment
+    cur.next(p);
+  }
+  // No copy may still be landing in shared memory when the CTA exits.
+  if (!ok && lane == 0)
+    for (int i = taken; i < issued; ++i) wait_drain(bars + 8 * (i % S), (i / S) & 1, 100000000ull);
+}
+
+// Joins the partial results of the segments that several pieces share (one warp per row):
+// with the pieces' m_i (log2 units), l_i and unnormalised O_i,
+//   m = max m_i,  l = sum 2^(m_i - m) l_i,  O = sum 2^(m_i - m) O_i / l,  LSE = (m + log2 l) ln 2.
+template <int D>
+__global__ void __launch_bounds__(256) fa_kv4_merge_kernel(const KV4DecodeParams p, int tile_rows) {
+  constexpr int kPer = D / 32;
+  const int lane = threadIdx.x % 32;
+  const long long row = static_cast<long long>(blockIdx.x) * 8 + threadIdx.x / 32;
+  if (row >= static_cast<long long>(p.B) * p.Hkv * p.R) return;
+  const long long bh = row / p.R;
+  const int r = static_cast<int>(row % p.R), b = static_cast<int>(bh / p.Hkv), kvh = static_cast<int>(bh % p.Hkv);
+  const int nblk = kv4_blocks(kv4_len(p, b));
+  if (nblk == 1) return;  // one block is never shared
+  const long long per = static_cast<long long>(p.Hkv) * p.row_tiles;
+  const long long T = p.lens ? kv4_blocks_before(p, p.B, lane) : p.B * per * nblk;
+  const long long first = (p.lens ? kv4_blocks_before(p, b, lane) : b * per * nblk) +
+                          static_cast<long long>(kvh * p.row_tiles + r / tile_rows) * nblk;
+  const int p0 = kv4_piece_of(T, p.pieces, first), p1 = kv4_piece_of(T, p.pieces, first + nblk - 1);
+  if (p0 == p1) return;  // written by its piece
+  // The piece in which the segment begins holds it in slot 1 unless it begins with it too, in
+  // which case it began nowhere before: slot 1 as well.  Later pieces hold it in slot 0.
+  auto slot = [&](int i) {
+    return p.part + ((static_cast<long long>(i) * 2 + (i == p0 ? 1 : 0)) * tile_rows + r % tile_rows) * (D + 2);
+  };
+  // With fewer blocks than pieces some pieces are empty and hold nothing.
+  auto empty = [&](int i) { return kv4_piece_begin(T, p.pieces, i) == kv4_piece_begin(T, p.pieces, i + 1); };
+  float m = -INFINITY;
+  for (int i = p0 + lane; i <= p1; i += 32)
+    if (!empty(i)) m = fmaxf(m, slot(i)[D]);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  const float mu = m == -INFINITY ? 0.f : m;
+  float l = 0.f, acc[kPer];
+#pragma unroll
+  for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+#pragma unroll 4
+  for (int i = p0; i <= p1; ++i) {
+    if (T < p.pieces && empty(i)) continue;
+    const float *src = slot(i);
+    const float f = ex2_approx(src[D] - mu);
+    l = fmaf(f, src[D + 1], l);
+#pragma unroll
+    for (int e = 0; e < kPer; e += 2) {
+      const float2 o = *reinterpret_cast<const float2 *>(src + lane * kPer + e);
+      acc[e] = fmaf(f, o.x, acc[e]);
+      acc[e + 1] = fmaf(f, o.y, acc[e + 1]);
     }
   }
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  uint32_t *dst = reinterpret_cast<uint32_t *>(p.o + row * D + lane * kPer);
+#pragma unroll
+  for (int e = 0; e < kPer; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+  if (lane == 0) p.lse[row] = l == 0.f ? -INFINITY : (mu + log2f(l)) * kLn2;
 }
 
 }  // namespace fa

@@ -403,9 +403,14 @@ int fa_kv4_read(const void *k_codes, const void *k_params, const void *v_codes,
  *   alibi_slopes: NULL, or DEVICE fp32 [Hq]: slope[h] * |i - j| is then taken off, with
  *        i = seqlens_k[b] - Nq + t the position of new row t and j that of the key.
  * What lies behind the last valid token of the cache is not looked at (it may be
- * uninitialised).  Rows that see no key get O = 0 and LSE = -inf.  Limits: (Hq / Hkv) * Nq
- * <= 128, B * Hkv <= 65535, num_splits in 1 .. 1024; workspace and num_splits as for
- * fa_decode, from the two functions below.
+ * uninitialised).  Rows that see no key get O = 0 and LSE = -inf.
+ *   num_splits: 1 .. 1024 pieces.  The blocks of 256 valid tokens of all batch entries and heads
+ *        are laid end to end and cut into that many equal pieces, one CTA each, so that
+ *        lengths that differ leave no SM idle; heads that several pieces share are joined by a
+ *        second kernel.  fa_decode_kv4_num_splits gives the library's choice.
+ *   workspace: device scratch of fa_decode_kv4_workspace_bytes() bytes, 16-byte aligned (may
+ *        be NULL when that is 0, i.e. num_splits == 1).
+ * Limit: (Hq / Hkv) * Nq <= 128.
  */
 int fa_decode_kv4(const void *q, const void *k_codes, const void *k_params, const void *v_codes,
                   const void *v_params, void *o, float *lse, const int *seqlens_k,

@@ -53,7 +53,7 @@ def _decode(**kw):
     (dict(softcap=float("inf")), fa.FA_ERR_INVALID_ARG), (dict(softcap=float("nan")), fa.FA_ERR_INVALID_ARG),
     (dict(d=80), fa.FA_ERR_UNSUPPORTED), (dict(cap=1000), fa.FA_ERR_UNSUPPORTED),
     (dict(Hq=8, Hkv=3), fa.FA_ERR_GQA), (dict(Hq=129, Hkv=1), fa.FA_ERR_UNSUPPORTED),
-    (dict(B=1 << 15, Hkv=2, Hq=2, cap=64), fa.FA_ERR_UNSUPPORTED),
+    (dict(B=1 << 24, Hkv=2, Hq=2, cap=64), fa.FA_ERR_UNSUPPORTED),
     (dict(ws=None), fa.FA_ERR_WORKSPACE), (dict(wsb=100), fa.FA_ERR_WORKSPACE),
     (dict(o=FAKE + 8), fa.FA_ERR_ALIGN), (dict(ws=FAKE + 8), fa.FA_ERR_ALIGN),
     (dict(lens=FAKE + 1), fa.FA_ERR_ALIGN), (dict(slopes=FAKE + 2), fa.FA_ERR_ALIGN),
@@ -71,10 +71,12 @@ def test_valid_arguments_without_a_device_report_cuda_error():
 
 def test_splits_and_workspace():
     pad = lambda x: (x + 255) // 256 * 256
-    rows, d = 2 * 8 * 3, 64
-    assert fa.fa_decode_kv4_workspace_bytes(2, 8, 2, 3, 1024, d, 1) == 0
-    assert fa.fa_decode_kv4_workspace_bytes(2, 8, 2, 3, 1024, d, 4) == pad(4 * rows * d * 4) + pad(4 * rows * 4)
-    assert fa.fa_decode_kv4_workspace_bytes(2, 8, 3, 3, 1024, d, 4) == 0
+    # two partial results a piece: O, m and l of a tile of 8 rows (16 where there are more, d < 256)
+    assert fa.fa_decode_kv4_workspace_bytes(2, 8, 2, 2, 1024, 64, 1) == 0
+    assert fa.fa_decode_kv4_workspace_bytes(2, 8, 2, 2, 1024, 64, 4) == pad(4 * 2 * 8 * 66 * 4)
+    assert fa.fa_decode_kv4_workspace_bytes(2, 8, 2, 3, 1024, 64, 4) == pad(4 * 2 * 16 * 66 * 4)
+    assert fa.fa_decode_kv4_workspace_bytes(2, 8, 2, 3, 1024, 256, 4) == pad(4 * 2 * 8 * 258 * 4)
+    assert fa.fa_decode_kv4_workspace_bytes(2, 8, 3, 3, 1024, 64, 4) == 0
     for B, Hq, Hkv, Nq, cap, dd in ((1, 1, 1, 1, 64, 64), (64, 32, 8, 1, 65536, 128), (1, 8, 8, 4, 1 << 20, 256)):
         assert 1 <= fa.fa_decode_kv4_num_splits(B, Hq, Hkv, Nq, cap, dd) <= 1024
     assert fa.fa_decode_kv4_num_splits(1, 8, 8, 1, 100, 128) == 0
