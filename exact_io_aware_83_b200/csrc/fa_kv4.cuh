@@ -203,9 +203,11 @@ __global__ void __launch_bounds__(256) fa_kv4_read_kernel(const KV4Params p) {
 // The R = (Hq / Hkv) Nq rows that share a K/V head are processed together, 8 NT at a time.
 //
 //  * q . k_j = sum_i (s_ji sum_{c in group i} q_c n_jc + m_ji sum_{c in group i} q_c): the
-//    codes go into the matrix product as whole numbers, exactly, and s, m are applied to the
-//    fp32 sums.  q is scaled by a power of two per row and converted to fp16 (8 significant
-//    bits of 11: exact but for entries below 2^-21 of the row's largest).
+//    codes go into the matrix product as whole numbers, exactly, and s is applied to the fp32
+//    sums.  q is scaled by a power of two per row and converted to fp16 (8 significant bits of
+//    11: exact but for entries below 2^-21 of the row's largest).  The second part is a product
+//    over the groups, the sums of q split in two fp16 numbers.  (e4m3 products, whose operand
+//    bytes the codes already are, measured slower: sm_100 runs the warp-level form as fp16.)
 //  * v_jc = m + n s in fp16 (one rounding, 2^-11 relative), p_j in fp16 (p_j <= 2^8).
 //  * The matrix products are warp-level m16n8k16: S^T = K Q^T with 16 keys as rows, O^T = V^T
 //    P^T with 16 channels as rows.  The codes are unpacked from registers straight into the
@@ -280,6 +282,20 @@ __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// The same with C = 0 (the sums of one group, or over the groups of 8 or 16).
+__device__ __forceinline__ void mma_f16_16816_z(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%10, %10, %10, %10};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
+__device__ __forceinline__ void mma_f16_1688_z(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%7, %7, %7, %7};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
@@ -298,11 +314,14 @@ __device__ __forceinline__ __half2 u32_h2(uint32_t u) { return *reinterpret_cast
 // The codes at bits 4 i .. 4 i + 3 of both halves of w, i = 0 (LOW) or 1, as fp16 whole
 // numbers: or-ed into the mantissa of 1024 (i = 0) or of 64 (i = 1, unit 2^-4), which is
 // then subtracted (exactly).
+// The two magic numbers live in registers (a three-input logic operation takes one immediate,
+// and the compiler would otherwise spend two of them).
 template <int I>
-__device__ __forceinline__ __half2 codes_h2(uint32_t w) {
+__device__ __forceinline__ __half2 codes_h2(uint32_t w, uint32_t magic) {
   constexpr uint32_t mask = I ? 0x00F000F0u : 0x000F000Fu;
-  constexpr uint32_t magic = I ? 0x54005400u : 0x64006400u;
-  return __hsub2(u32_h2((w & mask) | magic), u32_h2(magic));
+  uint32_t r;
+  asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "n"(mask), "r"(magic));  // (w & mask) | magic
+  return __hsub2(u32_h2(r), u32_h2(I ? 0x54005400u : 0x64006400u));
 }
 
 template <int D, int NT>
@@ -344,7 +363,7 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
 
 // A block of the line: its segment and its place in it.
 struct KV4Cursor {
-  int b, seg, blk, nblk, len;  // seg: kvh * row_tiles + row tile
+  int b, kvh, rt, blk, nblk, len;  // rt: row tile
   __device__ __forceinline__ void enter(const KV4DecodeParams &p, int b_) {
     b = b_;
     len = kv4_len(p, b);
@@ -353,8 +372,10 @@ struct KV4Cursor {
   __device__ __forceinline__ void next(const KV4DecodeParams &p) {
     if (++blk < nblk) return;
     blk = 0;
-    if (++seg < p.Hkv * p.row_tiles) return;
-    seg = 0;
+    if (++rt < p.row_tiles) return;
+    rt = 0;
+    if (++kvh < p.Hkv) return;
+    kvh = 0;
     if (b + 1 < p.B) enter(p, b + 1);
   }
 };
@@ -424,7 +445,8 @@ __global__ void __launch_bounds__(kKV4Warps * 32, KV4Layout<D, NT>::kCtas)
   int todo = misc[2];  // blocks left
   KV4Cursor cur;       // what is computed next
   cur.enter(p, misc[3]);
-  cur.seg = misc[4];
+  cur.kvh = misc[4] / p.row_tiles;
+  cur.rt = misc[4] % p.row_tiles;
   cur.blk = misc[5];
   KV4Cursor ahead = cur;  // what is loaded next
   int ahead_todo = todo, issued = 0, taken = 0;
@@ -438,7 +460,7 @@ __global__ void __launch_bounds__(kKV4Warps * 32, KV4Layout<D, NT>::kCtas)
       if (has && lane == 0) {
         const int st = issued % S;
         const uint32_t dst = ring + st * L::kStageBytes, bar = bars + 8 * st;
-        const long long row = static_cast<long long>(ahead.b * p.Hkv + ahead.seg / p.row_tiles) * p.cap + kb;
+        const long long row = static_cast<long long>(ahead.b * p.Hkv + ahead.kvh) * p.cap + kb;
         mbar_arrive_expect_tx(bar, L::kStageBytes);
         bulk_load(dst + L::kOffKC, p.kc + row * (D / 2), kKV4Keys * D / 2, bar);
         bulk_load(dst + L::kOffVC, p.vc + row * (D / 2), kKV4Keys * D / 2, bar);
@@ -456,6 +478,9 @@ __global__ void __launch_bounds__(kKV4Warps * 32, KV4Layout<D, NT>::kCtas)
 #pragma unroll 1
   for (int i = 0; i < S; ++i) issue();
 
+  uint32_t magic0, magic1;  // 1024 and 64, twice
+  asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic0));
+  asm volatile("mov.b32 %0, 0x54005400;" : "=r"(magic1));
   const int grp = p.R / p.Nq;  // query heads per K/V head
   const float inv_cap2 = p.softcap > 0.f ? 2.f * kLog2e / p.softcap : 0.f;
   const float cap_log2 = p.softcap * kLog2e;
@@ -466,14 +491,14 @@ __global__ void __launch_bounds__(kKV4Warps * 32, KV4Layout<D, NT>::kCtas)
     // ---- one segment, or the part of it that lies in this piece
     const int blk0 = cur.blk, count = min(cur.nblk - blk0, todo), len = cur.len;
     const bool began_before = blk0 > 0, ends_after = blk0 + count < cur.nblk;
-    const int kvh = cur.seg / p.row_tiles, r0 = (cur.seg % p.row_tiles) * ROWS;
+    const int kvh = cur.kvh, r0 = cur.rt * ROWS;
     const long long row0 = static_cast<long long>(cur.b * p.Hkv + kvh) * p.R + r0;
     const int pos0 = len - p.Nq;
 
     // Q fragments: row g of each 8-row tile, this lane's 8 channels of every group, scaled
     uint32_t qf[NT][G][4];         // [e]: channels (e, e + 4) of the word
+    uint32_t qs[NT][G == 8 ? 2 : 1];  // B operand of the product over the groups
     float fac[NT][2];              // rows 2c, 2c+1: scale (or scale log2 e without a cap) / row scaling
-    float qsum[NT][G][2];          // rows 2c, 2c+1: sum of the scaled q over each group
     float slope2[NT][2];
     int rpos[NT][2];               // position of the row
 #pragma unroll
@@ -496,6 +521,7 @@ __global__ void __launch_bounds__(kKV4Warps * 32, KV4Layout<D, NT>::kCtas)
       const int ex = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100);
       const float up = __uint_as_float(static_cast<uint32_t>(127 + 7 - ex) << 23);
       const float down = __uint_as_float(static_cast<uint32_t>(127 - 7 + ex) << 23);
+      float qsum[G];  // sums of the scaled q over each group
 #pragma unroll
       for (int i = 0; i < G; ++i) {
         float s = 0.f;
@@ -508,8 +534,27 @@ __global__ void __launch_bounds__(kKV4Warps * 32, KV4Layout<D, NT>::kCtas)
         for (int e = 0; e < 4; ++e) qf[nt][i][e] = pack_f16x2(x[i][e], x[i][e + 4]);
 #pragma unroll
         for (int o = 1; o < 4; o *= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
-        qsum[nt][i][0] = __shfl_sync(0xffffffffu, s, 8 * c);
-        qsum[nt][i][1] = __shfl_sync(0xffffffffu, s, 8 * c + 4);
+        qsum[i] = s;
+      }
+      // Row k of the operand: the sum of group k, its fp16 rounding first, then what is left
+      // (8 groups: in the second half of 16 rows; fewer: in rows G .. 2 G - 1 of 8).
+      {
+        constexpr int H = G == 8 ? 4 : G / 2;  // lanes that hold a pair of groups each
+        float a = 0.f, bq = 0.f;
+#pragma unroll
+        for (int i = 0; i < G; i += 2)
+          if (c % H == i / 2) {
+            a = qsum[i];
+            bq = qsum[i + 1];
+          }
+        const uint32_t hi = pack_f16x2(a, bq);
+        const uint32_t lo = pack_f16x2(a - __low2float(u32_h2(hi)), bq - __high2float(u32_h2(hi)));
+        if constexpr (G == 8) {
+          qs[nt][0] = hi;
+          qs[nt][1] = lo;
+        } else {
+          qs[nt][0] = c < H ? hi : (c < 2 * H ? lo : 0u);
+        }
       }
       const float f = (p.softcap > 0.f ? p.scale : p.sl2) * down;
       fac[nt][0] = __shfl_sync(0xffffffffu, f, 8 * c);
@@ -549,8 +594,7 @@ __global__ void __launch_bounds__(kKV4Warps * 32, KV4Layout<D, NT>::kCtas)
       float y[2][NT][4];  // [step][tile][key A: rows 2c, 2c+1; key B: rows 2c, 2c+1]
 #pragma unroll
       for (int st = 0; st < 2; ++st) {
-        uint32_t w[2][KW];
-        uint32_t par[2][G];  // s of the groups in pairs, then m in pairs
+        uint32_t w[2][KW], sc[2][G / 2], mn[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int key = 16 * st + ka + 8 * e;
@@ -558,48 +602,41 @@ __global__ void __launch_bounds__(kKV4Warps * 32, KV4Layout<D, NT>::kCtas)
           const uint32_t *ps = reinterpret_cast<const uint32_t *>(stage + L::kOffKP + key * (4 * G));
           if constexpr (KW == 2) {
             *reinterpret_cast<uint2 *>(w[e]) = *reinterpret_cast<const uint2 *>(src);
-            *reinterpret_cast<uint2 *>(par[e]) = *reinterpret_cast<const uint2 *>(ps);
+            sc[e][0] = ps[0];
           } else {
 #pragma unroll
-            for (int i = 0; i < KW; i += 4) {
-              *reinterpret_cast<uint4 *>(w[e] + i) = *reinterpret_cast<const uint4 *>(src + i);
-              *reinterpret_cast<uint4 *>(par[e] + i) = *reinterpret_cast<const uint4 *>(ps + i);
-            }
+            for (int i = 0; i < KW; i += 4) *reinterpret_cast<uint4 *>(w[e] + i) = *reinterpret_cast<const uint4 *>(src + i);
+            if constexpr (KW == 4) *reinterpret_cast<uint2 *>(sc[e]) = *reinterpret_cast<const uint2 *>(ps);
+            else *reinterpret_cast<uint4 *>(sc[e]) = *reinterpret_cast<const uint4 *>(ps);
           }
+          mn[e] = ps[G / 2 + (G == 8 ? c : c % (G / 2))];
         }
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) y[st][nt][e] = 0.f;
+        for (int nt = 0; nt < NT; ++nt) {
+          if constexpr (G == 8) mma_f16_16816_z(y[st][nt], mn[0], mn[1], mn[0], mn[1], qs[nt][0], qs[nt][1]);
+          else mma_f16_1688_z(y[st][nt], mn[0], mn[1], qs[nt][0]);
+        }
 #pragma unroll
         for (int i = 0; i < G; ++i) {
-          float part[NT][4];
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) part[nt][e] = 0.f;
           uint32_t a[2][4];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            a[e][0] = h2_u32(codes_h2<0>(w[e][i]));
-            a[e][1] = h2_u32(codes_h2<1>(w[e][i]));
-            a[e][2] = h2_u32(codes_h2<0>(w[e][i] >> 8));
-            a[e][3] = h2_u32(codes_h2<1>(w[e][i] >> 8));
+            a[e][0] = h2_u32(codes_h2<0>(w[e][i], magic0));
+            a[e][1] = h2_u32(codes_h2<1>(w[e][i], magic1));
+            a[e][2] = h2_u32(codes_h2<0>(w[e][i] >> 8, magic0));
+            a[e][3] = h2_u32(codes_h2<1>(w[e][i] >> 8, magic1));
           }
+          auto pick = [](uint32_t u, int hi) { return hi ? __high2float(u32_h2(u)) : __low2float(u32_h2(u)); };
+          const float sA = pick(sc[0][i / 2], i & 1), sB = pick(sc[1][i / 2], i & 1);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            mma_f16_16816(part[nt], a[0][0], a[1][0], a[0][1], a[1][1], qf[nt][i][0], qf[nt][i][1]);
-            mma_f16_16816(part[nt], a[0][2], a[1][2], a[0][3], a[1][3], qf[nt][i][2], qf[nt][i][3]);
-          }
-          auto pick = [](uint32_t u, int hi) { return __half2float(hi ? __high2half(u32_h2(u)) : __low2half(u32_h2(u))); };
-          const float sA = pick(par[0][i / 2], i & 1), sB = pick(par[1][i / 2], i & 1);
-          const float mA = pick(par[0][G / 2 + i / 2], i & 1), mB = pick(par[1][G / 2 + i / 2], i & 1);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            y[st][nt][0] = fmaf(sA, part[nt][0], fmaf(mA, qsum[nt][i][0], y[st][nt][0]));
-            y[st][nt][1] = fmaf(sA, part[nt][1], fmaf(mA, qsum[nt][i][1], y[st][nt][1]));
-            y[st][nt][2] = fmaf(sB, part[nt][2], fmaf(mB, qsum[nt][i][0], y[st][nt][2]));
-            y[st][nt][3] = fmaf(sB, part[nt][3], fmaf(mB, qsum[nt][i][1], y[st][nt][3]));
+            float part[4];
+            mma_f16_16816_z(part, a[0][0], a[1][0], a[0][1], a[1][1], qf[nt][i][0], qf[nt][i][1]);
+            mma_f16_16816(part, a[0][2], a[1][2], a[0][3], a[1][3], qf[nt][i][2], qf[nt][i][3]);
+            y[st][nt][0] = fmaf(sA, part[0], y[st][nt][0]);
+            y[st][nt][1] = fmaf(sA, part[1], y[st][nt][1]);
+            y[st][nt][2] = fmaf(sB, part[2], y[st][nt][2]);
+            y[st][nt][3] = fmaf(sB, part[3], y[st][nt][3]);
           }
         }
         // ---- cap, bias, mask: the scores in log2 units
@@ -664,6 +701,11 @@ __global__ void __launch_bounds__(kKV4Warps * 32, KV4Layout<D, NT>::kCtas)
             for (int e = 0; e < 4; ++e) acc[i][nt][e] *= alpha[e & 1];
         }
       }
+      float mu[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) mu[nt][e] = m_run[nt][e] == -INFINITY ? 0.f : m_run[nt][e];
 #pragma unroll
       for (int st = 0; st < 2; ++st) {
         uint32_t pb[NT][2];
@@ -672,8 +714,7 @@ __global__ void __launch_bounds__(kKV4Warps * 32, KV4Layout<D, NT>::kCtas)
           float pr[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const float mu = m_run[nt][e & 1] == -INFINITY ? 0.f : m_run[nt][e & 1];
-            pr[e] = ex2_approx(y[st][nt][e] - mu);
+            pr[e] = ex2_approx(y[st][nt][e] - mu[nt][e & 1]);
             l_run[nt][e & 1] += pr[e];
           }
           pb[nt][0] = movmatrix_trans(pack_f16x2(pr[0], pr[1]));
@@ -711,10 +752,10 @@ __global__ void __launch_bounds__(kKV4Warps * 32, KV4Layout<D, NT>::kCtas)
 #pragma unroll
             for (int t = 0; t < 2; ++t) {
               const uint32_t x0 = t ? x[0] >> 8 : x[0], x1 = t ? x[1] >> 8 : x[1];
-              const uint32_t a0 = h2_u32(__hfma2(codes_h2<0>(x0), sp[0], mp[0]));
-              const uint32_t a1 = h2_u32(__hfma2(codes_h2<1>(x0), sp[0], mp[0]));
-              const uint32_t a2 = h2_u32(__hfma2(codes_h2<0>(x1), sp[1], mp[1]));
-              const uint32_t a3 = h2_u32(__hfma2(codes_h2<1>(x1), sp[1], mp[1]));
+              const uint32_t a0 = h2_u32(__hfma2(codes_h2<0>(x0, magic0), sp[0], mp[0]));
+              const uint32_t a1 = h2_u32(__hfma2(codes_h2<1>(x0, magic1), sp[0], mp[0]));
+              const uint32_t a2 = h2_u32(__hfma2(codes_h2<0>(x1, magic0), sp[1], mp[1]));
+              const uint32_t a3 = h2_u32(__hfma2(codes_h2<1>(x1, magic1), sp[1], mp[1]));
 #pragma unroll
               for (int nt = 0; nt < NT; ++nt)
                 mma_f16_16816(acc[w * 4 + half * 2 + t][nt], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
