@@ -201,11 +201,16 @@ bool device_ready() {
     ok = ok && set_smem(fa::fa_decode_kernel<256, 16, true>, fa::DecodeLayout<256, 16>::kSmemBytes);
     ok = ok && set_smem(fa::fa_decode_kernel<256, 32, true>, fa::DecodeLayout<256, 32>::kSmemBytes);
     ok = ok && set_smem(fa::fa_decode_kernel<256, 64, true>, fa::DecodeLayout<256, 64>::kSmemBytes);
-    ok = ok && set_smem(fa::fa_decode_kv4_kernel<64, 1>, fa::KV4Layout<64, 1>::kSmemBytes);
-    ok = ok && set_smem(fa::fa_decode_kv4_kernel<64, 2>, fa::KV4Layout<64, 2>::kSmemBytes);
-    ok = ok && set_smem(fa::fa_decode_kv4_kernel<128, 1>, fa::KV4Layout<128, 1>::kSmemBytes);
-    ok = ok && set_smem(fa::fa_decode_kv4_kernel<128, 2>, fa::KV4Layout<128, 2>::kSmemBytes);
-    ok = ok && set_smem(fa::fa_decode_kv4_kernel<256, 1>, fa::KV4Layout<256, 1>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kv4_kernel<64, 1, false>, fa::KV4Layout<64, 1>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kv4_kernel<64, 1, true>, fa::KV4Layout<64, 1>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kv4_kernel<64, 2, false>, fa::KV4Layout<64, 2>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kv4_kernel<64, 2, true>, fa::KV4Layout<64, 2>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kv4_kernel<128, 1, false>, fa::KV4Layout<128, 1>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kv4_kernel<128, 1, true>, fa::KV4Layout<128, 1>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kv4_kernel<128, 2, false>, fa::KV4Layout<128, 2>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kv4_kernel<128, 2, true>, fa::KV4Layout<128, 2>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kv4_kernel<256, 1, false>, fa::KV4Layout<256, 1>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kv4_kernel<256, 1, true>, fa::KV4Layout<256, 1>::kSmemBytes);
     using fa::FwdPLayout;
     ok = ok && set_smem(fa::fa_fwd_persist_kernel<64, fa::kAttnFull>, FwdPLayout<64>::kSmemBytes);
     ok = ok && set_smem(fa::fa_fwd_persist_kernel<64, fa::kAttnCausal>, FwdPLayout<64>::kSmemBytes);
@@ -468,8 +473,12 @@ size_t kv4_workspace(int R, int d, int pieces) {
 
 template <int D, int NT>
 void launch_kv4(const fa::KV4DecodeParams &p, cudaStream_t s) {
-  fa::fa_decode_kv4_kernel<D, NT>
-      <<<static_cast<unsigned>(p.pieces), fa::kKV4Warps * 32, fa::KV4Layout<D, NT>::kSmemBytes, s>>>(p);
+  constexpr int smem = fa::KV4Layout<D, NT>::kSmemBytes;
+  const unsigned grid = static_cast<unsigned>(p.pieces);
+  if (p.softcap > 0.f || p.slopes)
+    fa::fa_decode_kv4_kernel<D, NT, true><<<grid, fa::kKV4Warps * 32, smem, s>>>(p);
+  else
+    fa::fa_decode_kv4_kernel<D, NT, false><<<grid, fa::kKV4Warps * 32, smem, s>>>(p);
 }
 
 // Launches the forward kernel for d (maps and parameters prepared by the caller).

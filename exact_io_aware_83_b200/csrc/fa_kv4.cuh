@@ -205,7 +205,7 @@ __global__ void __launch_bounds__(256) fa_kv4_read_kernel(const KV4Params p) {
 //  * q . k_j = sum_i (s_ji sum_{c in group i} q_c n_jc + m_ji sum_{c in group i} q_c): the
 //    codes go into the matrix product as whole numbers, exactly, and s is applied to the fp32
 //    sums.  q is scaled by a power of two per row and converted to fp16 (8 significant bits of
-//    11: exact but for entries below 2^-21 of the row's largest).  The second part is a product
+//    11: exact but for entries below 2^-20 of the row's largest).  The second part is a product
 //    over the groups, the sums of q split in two fp16 numbers.  (e4m3 products, whose operand
 //    bytes the codes already are, measured slower: sm_100 runs the warp-level form as fp16.)
 //  * v_jc = m + n s in fp16 (one rounding, 2^-11 relative), p_j in fp16 (p_j <= 2^8).
@@ -220,9 +220,9 @@ __global__ void __launch_bounds__(256) fa_kv4_read_kernel(const KV4Params p) {
 //    into `pieces` equal ranges, one CTA each, so that lengths that differ leave no SM idle.
 //    A segment that lies inside one piece is written by its CTA; one that several pieces
 //    share leaves a partial result per piece in the workspace, which fa_kv4_merge_kernel joins.
-//  * Each warp takes 32 keys of a block and streams its own tiles, across segments, through a
-//    ring of shared-memory stages filled by bulk copies (the rows of one head are contiguous);
-//    warps meet only where a segment ends.
+//  * Blocks stream through a ring of shared-memory stages, across segments, four bulk copies
+//    each (the rows of one head are contiguous); every warp takes 32 keys of a block, and the
+//    warps take turns at refilling the stage that all have left.
 struct KV4DecodeParams {
   const __nv_bfloat16 *q;  // [B, Hq, Nq, D]
   const uint8_t *kc, *vc;
@@ -290,12 +290,6 @@ __device__ __forceinline__ void mma_f16_16816_z(float (&d)[4], uint32_t a0, uint
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
-__device__ __forceinline__ void mma_f16_1688_z(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%7, %7, %7, %7};"
-      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a0), "r"(a1), "r"(b0), "f"(0.f));
-}
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
   uint32_t r;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
@@ -317,11 +311,15 @@ __device__ __forceinline__ __half2 u32_h2(uint32_t u) { return *reinterpret_cast
 // The two magic numbers live in registers (a three-input logic operation takes one immediate,
 // and the compiler would otherwise spend two of them).
 template <int I>
-__device__ __forceinline__ __half2 codes_h2(uint32_t w, uint32_t magic) {
+__device__ __forceinline__ uint32_t codes_biased(uint32_t w, uint32_t magic) {
   constexpr uint32_t mask = I ? 0x00F000F0u : 0x000F000Fu;
   uint32_t r;
   asm("lop3.b32 %0, %1, %2, %3, 0xEA;" : "=r"(r) : "r"(w), "n"(mask), "r"(magic));  // (w & mask) | magic
-  return __hsub2(u32_h2(r), u32_h2(I ? 0x54005400u : 0x64006400u));
+  return r;
+}
+template <int I>
+__device__ __forceinline__ __half2 codes_h2(uint32_t w, uint32_t magic) {
+  return __hsub2(u32_h2(codes_biased<I>(w, magic)), u32_h2(I ? 0x54005400u : 0x64006400u));
 }
 
 template <int D, int NT>
@@ -332,20 +330,20 @@ struct KV4Layout {
   static constexpr int MT = VW * 4;   // 16-channel tiles of O^T
   static constexpr int ROWS = 8 * NT;
   static constexpr int kCtas = NT == 1 && D <= 128 ? 2 : 1;  // CTAs per SM
-  // One stage of a warp's ring: codes and params of 32 keys.
+  // One stage of the ring: codes and params of a block.
   static constexpr int kOffKC = 0;
-  static constexpr int kOffVC = kOffKC + kKV4Keys * D / 2;
-  static constexpr int kOffKP = kOffVC + kKV4Keys * D / 2;
-  static constexpr int kOffVP = kOffKP + kKV4Keys * 4 * G;
-  static constexpr int kStageBytes = kOffVP + kKV4Keys * 4 * G;
+  static constexpr int kOffVC = kOffKC + kKV4Block * D / 2;
+  static constexpr int kOffKP = kOffVC + kKV4Block * D / 2;
+  static constexpr int kOffVP = kOffKP + kKV4Block * 4 * G;
+  static constexpr int kStageBytes = kOffVP + kKV4Block * 4 * G;
   static constexpr int kPartBytes = kKV4Warps / 2 * ROWS * D * 4;  // O of half the warps, where a segment ends
-  static constexpr int kFixed = kPartBytes + 2 * kKV4Warps * ROWS * 4 + kKV4Warps * 8 * 8 + 64 + 128;
-  static constexpr int kFit = ((kCtas == 2 ? 232448 / 2 - 1024 : 232448) - kFixed) / (kKV4Warps * kStageBytes);
+  static constexpr int kFixed = kPartBytes + 2 * kKV4Warps * ROWS * 4 + 2 * 8 * 8 + 64 + 128;
+  static constexpr int kFit = ((kCtas == 2 ? 232448 / 2 - 1024 : 232448) - kFixed) / kStageBytes;
   static constexpr int kStages = kFit > 4 ? 4 : kFit;
-  static constexpr int kOffPart = kKV4Warps * kStages * kStageBytes;
+  static constexpr int kOffPart = kStages * kStageBytes;
   static constexpr int kOffM = kOffPart + kPartBytes;      // [warp][row] m, then l
-  static constexpr int kOffBar = kOffM + 2 * kKV4Warps * ROWS * 4;
-  static constexpr int kOffMisc = kOffBar + kKV4Warps * 8 * 8;
+  static constexpr int kOffBar = kOffM + 2 * kKV4Warps * ROWS * 4;  // full[8], empty[8]
+  static constexpr int kOffMisc = kOffBar + 2 * 8 * 8;
   static constexpr int kSmemBytes = kOffMisc + 64 + 128;   // + slack for 128-byte alignment
   static_assert(kStages >= 2 && kStages <= 8, "ring");
 };
@@ -380,7 +378,7 @@ struct KV4Cursor {
   }
 };
 
-template <int D, int NT>
+template <int D, int NT, bool CHANGED>  // CHANGED: capped scores or a distance bias
 __global__ void __launch_bounds__(kKV4Warps * 32, KV4Layout<D, NT>::kCtas)
     fa_decode_kv4_kernel(const KV4DecodeParams p) {
   using L = KV4Layout<D, NT>;
@@ -390,18 +388,20 @@ __global__ void __launch_bounds__(kKV4Warps * 32, KV4Layout<D, NT>::kCtas)
   uint8_t *smem = smem_raw + (base - smem_u32(smem_raw));
   float *sm_o = reinterpret_cast<float *>(smem + L::kOffPart);
   float *sm_m = reinterpret_cast<float *>(smem + L::kOffM), *sm_l = sm_m + kKV4Warps * ROWS;
-  int *misc = reinterpret_cast<int *>(smem + L::kOffMisc);  // [0] abort flag, [2..] line
+  // [0] abort flag, [1] blocks whose copies have been started, [2..5] the piece, [6..11] what is loaded next
+  int *misc = reinterpret_cast<int *>(smem + L::kOffMisc);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int g = lane / 4, c = lane % 4;
-  const uint32_t ring = base + warp * (S * L::kStageBytes);
-  uint8_t *ring_ptr = smem + warp * (S * L::kStageBytes);
-  const uint32_t bars = base + L::kOffBar + warp * 64;
+  const uint32_t full = base + L::kOffBar, empty = full + 64;
   volatile int *abort_flag = misc;
 
   // ---- this piece of the line: blocks [x0, x1), and the segment that x0 lies in
-  if (lane < S) mbar_init(bars + 8 * lane, 1);
-  fence_mbar_init();
+  if (threadIdx.x < S) {
+    mbar_init(full + 8 * threadIdx.x, 1);
+    mbar_init(empty + 8 * threadIdx.x, kKV4Warps);
+    fence_mbar_init();
+  }
   if (warp == 0) {
     const long long per = static_cast<long long>(p.Hkv) * p.row_tiles;
     long long T;
@@ -434,49 +434,53 @@ __global__ void __launch_bounds__(kKV4Warps * 32, KV4Layout<D, NT>::kCtas)
     if (lane == 0) {
       const int nblk = kv4_blocks(kv4_len(p, b));
       const long long in = x0 - before;
-      misc[0] = 0;
+      misc[0] = misc[1] = 0;
       misc[2] = static_cast<int>(x1 - x0);
       misc[3] = b;
       misc[4] = static_cast<int>(in / nblk);
       misc[5] = static_cast<int>(in % nblk);
+      KV4Cursor *ahead = reinterpret_cast<KV4Cursor *>(misc + 6);
+      ahead->enter(p, b);
+      ahead->kvh = misc[4] / p.row_tiles;
+      ahead->rt = misc[4] % p.row_tiles;
+      ahead->blk = misc[5];
     }
   }
   __syncthreads();
-  int todo = misc[2];  // blocks left
-  KV4Cursor cur;       // what is computed next
+  const int total = misc[2];  // blocks of the piece
+  int todo = total, taken = 0;
+  KV4Cursor cur;              // what is computed next
   cur.enter(p, misc[3]);
   cur.kvh = misc[4] / p.row_tiles;
   cur.rt = misc[4] % p.row_tiles;
   cur.blk = misc[5];
-  KV4Cursor ahead = cur;  // what is loaded next
-  int ahead_todo = todo, issued = 0, taken = 0;
   bool ok = true;
 
-  // Starts the copies of this warp's next tile that has keys, if any is left.
+  // Starts the copies of the piece's next block (one thread; the cursor passes from one issuer
+  // to the next through the barriers of the stage).
   auto issue = [&]() {
-    while (ahead_todo > 0) {
-      const int kb = ahead.blk * kKV4Block + warp * kKV4Keys;
-      const bool has = kb < ahead.len;
-      if (has && lane == 0) {
-        const int st = issued % S;
-        const uint32_t dst = ring + st * L::kStageBytes, bar = bars + 8 * st;
-        const long long row = static_cast<long long>(ahead.b * p.Hkv + ahead.kvh) * p.cap + kb;
-        mbar_arrive_expect_tx(bar, L::kStageBytes);
-        bulk_load(dst + L::kOffKC, p.kc + row * (D / 2), kKV4Keys * D / 2, bar);
-        bulk_load(dst + L::kOffVC, p.vc + row * (D / 2), kKV4Keys * D / 2, bar);
-        bulk_load(dst + L::kOffKP, p.kp + row * (2 * G), kKV4Keys * 4 * G, bar);
-        bulk_load(dst + L::kOffVP, p.vp + row * (2 * G), kKV4Keys * 4 * G, bar);
-      }
-      ahead.next(p);
-      --ahead_todo;
-      if (has) {
-        ++issued;
-        return;
-      }
+    KV4Cursor *ahead = reinterpret_cast<KV4Cursor *>(misc + 6);
+    KV4Cursor a = *ahead;
+    const int st = misc[1] % S;
+    const uint32_t dst = base + st * L::kStageBytes, bar = full + 8 * st;
+    const int kb = a.blk * kKV4Block;
+    const int n = min(kKV4Block, (a.len - kb + kKV4Keys - 1) / kKV4Keys * kKV4Keys);  // within cap, a multiple of 64
+    if (n > 0) {
+      const long long row = static_cast<long long>(a.b * p.Hkv + a.kvh) * p.cap + kb;
+      mbar_arrive_expect_tx(bar, static_cast<uint32_t>(n) * (D + 8 * G));
+      bulk_load(dst + L::kOffKC, p.kc + row * (D / 2), n * (D / 2), bar);
+      bulk_load(dst + L::kOffVC, p.vc + row * (D / 2), n * (D / 2), bar);
+      bulk_load(dst + L::kOffKP, p.kp + row * (2 * G), n * (4 * G), bar);
+      bulk_load(dst + L::kOffVP, p.vp + row * (2 * G), n * (4 * G), bar);
+    } else {
+      mbar_arrive(bar);  // a segment without keys
     }
+    a.next(p);
+    *ahead = a;
+    ++misc[1];
   };
-#pragma unroll 1
-  for (int i = 0; i < S; ++i) issue();
+  if (threadIdx.x == 0)
+    for (int i = 0; i < min(S, total); ++i) issue();
 
   uint32_t magic0, magic1;  // 1024 and 64, twice
   asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic0));
@@ -497,8 +501,8 @@ __global__ void __launch_bounds__(kKV4Warps * 32, KV4Layout<D, NT>::kCtas)
 
     // Q fragments: row g of each 8-row tile, this lane's 8 channels of every group, scaled
     uint32_t qf[NT][G][4];         // [e]: channels (e, e + 4) of the word
-    uint32_t qs[NT][G == 8 ? 2 : 1];  // B operand of the product over the groups
-    float fac[NT][2];              // rows 2c, 2c+1: scale (or scale log2 e without a cap) / row scaling
+    uint32_t qs[NT][G == 8 ? 4 : 2];  // B operand of the product over the groups
+    float raw[NT][2], fac[NT][2];  // rows 2c, 2c+1: from the products to scores, and from those to log2
     float slope2[NT][2];
     int rpos[NT][2];               // position of the row
 #pragma unroll
@@ -517,48 +521,65 @@ __global__ void __launch_bounds__(kKV4Warps * 32, KV4Layout<D, NT>::kCtas)
       }
 #pragma unroll
       for (int o = 1; o < 4; o *= 2) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-      // largest magnitude into [128, 256)
+      // largest magnitude into [8, 16): 64 times the sum of 16 of them stays inside fp16
       const int ex = max(static_cast<int>(__float_as_uint(amax) >> 23) - 127, -100);
-      const float up = __uint_as_float(static_cast<uint32_t>(127 + 7 - ex) << 23);
-      const float down = __uint_as_float(static_cast<uint32_t>(127 - 7 + ex) << 23);
-      float qsum[G];  // sums of the scaled q over each group
+      const float up = __uint_as_float(static_cast<uint32_t>(127 + 3 - ex) << 23);
+      const float down = __uint_as_float(static_cast<uint32_t>(127 - 3 + ex) << 23);
+      float qsum[G], qodd[G];  // sums of the scaled q over each group, and -64 times those of pairs 1 and 3
 #pragma unroll
       for (int i = 0; i < G; ++i) {
         float s = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          x[i][e] *= up;
-          s += x[i][e];
-        }
+        for (int e = 0; e < 8; ++e) x[i][e] *= up;
+        float odd = (x[i][1] + x[i][3]) + (x[i][5] + x[i][7]);
+        s = odd + ((x[i][0] + x[i][2]) + (x[i][4] + x[i][6]));
 #pragma unroll
         for (int e = 0; e < 4; ++e) qf[nt][i][e] = pack_f16x2(x[i][e], x[i][e + 4]);
 #pragma unroll
-        for (int o = 1; o < 4; o *= 2) s += __shfl_xor_sync(0xffffffffu, s, o);
+        for (int o = 1; o < 4; o *= 2) {
+          s += __shfl_xor_sync(0xffffffffu, s, o);
+          odd += __shfl_xor_sync(0xffffffffu, odd, o);
+        }
         qsum[i] = s;
+        qodd[i] = -64.f * odd;
       }
-      // Row k of the operand: the sum of group k, its fp16 rounding first, then what is left
-      // (8 groups: in the second half of 16 rows; fewer: in rows G .. 2 G - 1 of 8).
+      // Row k of the operand that meets the groups' m: the sum of group k, its fp16 rounding
+      // first, then what is left (8 groups: in the second half of 16 rows; fewer: in rows
+      // G .. 2 G - 1 of 8).  The rows that meet s hold the other sums the same way.
       {
         constexpr int H = G == 8 ? 4 : G / 2;  // lanes that hold a pair of groups each
-        float a = 0.f, bq = 0.f;
+        float a = 0.f, bq = 0.f, ao = 0.f, bo = 0.f;
 #pragma unroll
         for (int i = 0; i < G; i += 2)
           if (c % H == i / 2) {
             a = qsum[i];
             bq = qsum[i + 1];
+            ao = qodd[i];
+            bo = qodd[i + 1];
           }
-        const uint32_t hi = pack_f16x2(a, bq);
-        const uint32_t lo = pack_f16x2(a - __low2float(u32_h2(hi)), bq - __high2float(u32_h2(hi)));
+        auto split = [&](float u, float v, uint32_t &hi, uint32_t &lo) {
+          hi = pack_f16x2(u, v);
+          lo = pack_f16x2(u - __low2float(u32_h2(hi)), v - __high2float(u32_h2(hi)));
+        };
+        uint32_t hi, lo, hi_o, lo_o;
+        split(a, bq, hi, lo);
+        split(ao, bo, hi_o, lo_o);
         if constexpr (G == 8) {
           qs[nt][0] = hi;
           qs[nt][1] = lo;
+          qs[nt][2] = hi_o;
+          qs[nt][3] = lo_o;
         } else {
           qs[nt][0] = c < H ? hi : (c < 2 * H ? lo : 0u);
+          qs[nt][1] = c < H ? hi_o : (c < 2 * H ? lo_o : 0u);
         }
       }
-      const float f = (p.softcap > 0.f ? p.scale : p.sl2) * down;
-      fac[nt][0] = __shfl_sync(0xffffffffu, f, 8 * c);
-      fac[nt][1] = __shfl_sync(0xffffffffu, f, 8 * c + 4);
+      // (never 0: hidden scores are -inf and stay so)
+      const float f = fmaxf((p.softcap > 0.f ? p.scale : p.sl2) * down, 1e-37f);
+      raw[nt][0] = __shfl_sync(0xffffffffu, f, 8 * c);
+      raw[nt][1] = __shfl_sync(0xffffffffu, f, 8 * c + 4);
+      fac[nt][0] = CHANGED ? 1.f : raw[nt][0];
+      fac[nt][1] = CHANGED ? 1.f : raw[nt][1];
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int rr = r0 + nt * 8 + 2 * c + e;
@@ -582,24 +603,28 @@ __global__ void __launch_bounds__(kKV4Warps * 32, KV4Layout<D, NT>::kCtas)
       l_run[nt][0] = l_run[nt][1] = 0.f;
     }
 
+    int kb = blk0 * kKV4Block + warp * kKV4Keys;
 #pragma unroll 1
-    for (int blk = blk0; blk < blk0 + count; ++blk) {
-      const int kb = blk * kKV4Block + warp * kKV4Keys;
-      if (kb >= len) continue;
+    for (int i = 0; i < count; ++i, ++taken, kb += kKV4Block) {
+      // The stage that the block before this one was in is refilled, by one warp in turn.
+      if (taken > 0 && taken + S - 1 < total && warp == taken % kKV4Warps && lane == 0 &&
+          wait_bounded(empty + 8 * ((taken - 1) % S), ((taken - 1) / S) & 1, abort_flag, wait_site(5, 8 + (taken - 1) % S, taken)))
+        issue();
+      __syncwarp();
       const int st_ = taken % S;
-      if (ok) ok = warp_wait_bounded(bars + 8 * st_, (taken / S) & 1, abort_flag, wait_site(5, st_, taken));
-      if (!ok) continue;  // the flag is up: nothing of this call is valid any more
-      ++taken;
-      const uint8_t *stage = ring_ptr + st_ * L::kStageBytes;
+      if (ok) ok = warp_wait_bounded(full + 8 * st_, (taken / S) & 1, abort_flag, wait_site(5, st_, taken));
+      if (ok && kb < len) {  // !ok: the flag is up, nothing of this call is valid any more
+      const uint8_t *stage = smem + st_ * L::kStageBytes + warp * (kKV4Keys * D / 2);
+      const uint8_t *stage_par = smem + st_ * L::kStageBytes + L::kOffKP + warp * (kKV4Keys * 4 * G);
       float y[2][NT][4];  // [step][tile][key A: rows 2c, 2c+1; key B: rows 2c, 2c+1]
 #pragma unroll
       for (int st = 0; st < 2; ++st) {
-        uint32_t w[2][KW], sc[2][G / 2], mn[2];
+        uint32_t w[2][KW], sc[2][G / 2], mn[2], sn[2];
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int key = 16 * st + ka + 8 * e;
           const uint32_t *src = reinterpret_cast<const uint32_t *>(stage + L::kOffKC + key * (D / 2)) + c * KW;
-          const uint32_t *ps = reinterpret_cast<const uint32_t *>(stage + L::kOffKP + key * (4 * G));
+          const uint32_t *ps = reinterpret_cast<const uint32_t *>(stage_par + key * (4 * G));
           if constexpr (KW == 2) {
             *reinterpret_cast<uint2 *>(w[e]) = *reinterpret_cast<const uint2 *>(src);
             sc[e][0] = ps[0];
@@ -610,21 +635,26 @@ __global__ void __launch_bounds__(kKV4Warps * 32, KV4Layout<D, NT>::kCtas)
             else *reinterpret_cast<uint4 *>(sc[e]) = *reinterpret_cast<const uint4 *>(ps);
           }
           mn[e] = ps[G / 2 + (G == 8 ? c : c % (G / 2))];
+          sn[e] = ps[G == 8 ? c : c % (G / 2)];
         }
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          if constexpr (G == 8) mma_f16_16816_z(y[st][nt], mn[0], mn[1], mn[0], mn[1], qs[nt][0], qs[nt][1]);
-          else mma_f16_1688_z(y[st][nt], mn[0], mn[1], qs[nt][0]);
+          if constexpr (G == 8) {
+            mma_f16_16816_z(y[st][nt], mn[0], mn[1], mn[0], mn[1], qs[nt][0], qs[nt][1]);
+            mma_f16_16816(y[st][nt], sn[0], sn[1], sn[0], sn[1], qs[nt][2], qs[nt][3]);
+          } else {
+            mma_f16_16816_z(y[st][nt], mn[0], mn[1], sn[0], sn[1], qs[nt][0], qs[nt][1]);
+          }
         }
 #pragma unroll
         for (int i = 0; i < G; ++i) {
-          uint32_t a[2][4];
+          uint32_t a[2][4];  // pairs 1 and 3 stay 64 too large; the product over the groups takes that off
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             a[e][0] = h2_u32(codes_h2<0>(w[e][i], magic0));
-            a[e][1] = h2_u32(codes_h2<1>(w[e][i], magic1));
+            a[e][1] = codes_biased<1>(w[e][i], magic1);
             a[e][2] = h2_u32(codes_h2<0>(w[e][i] >> 8, magic0));
-            a[e][3] = h2_u32(codes_h2<1>(w[e][i] >> 8, magic1));
+            a[e][3] = codes_biased<1>(w[e][i] >> 8, magic1);
           }
           auto pick = [](uint32_t u, int hi) { return hi ? __high2float(u32_h2(u)) : __low2float(u32_h2(u)); };
           const float sA = pick(sc[0][i / 2], i & 1), sB = pick(sc[1][i / 2], i & 1);
@@ -639,26 +669,20 @@ __global__ void __launch_bounds__(kKV4Warps * 32, KV4Layout<D, NT>::kCtas)
             y[st][nt][3] = fmaf(sB, part[3], y[st][nt][3]);
           }
         }
-        // ---- cap, bias, mask: the scores in log2 units
+      }
+      // ---- cap and bias: the scores in log2 units (without them the factor goes into the exponent)
+      if constexpr (CHANGED) {
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) y[st][nt][e] *= fac[nt][e & 1];
-        if (p.softcap > 0.f) {
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e) y[st][nt][e] = softcap_log2(y[st][nt][e], inv_cap2, cap_log2);
-        }
-        if (p.slopes) {
+        for (int st = 0; st < 2; ++st)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
+              float v = y[st][nt][e] * raw[nt][e & 1];
+              if (p.softcap > 0.f) v = softcap_log2(v, inv_cap2, cap_log2);
               const int key = kb + 16 * st + ka + 8 * (e / 2);
-              y[st][nt][e] = fmaf(-slope2[nt][e & 1], fabsf(static_cast<float>(rpos[nt][e & 1] - key)), y[st][nt][e]);
+              y[st][nt][e] = fmaf(-slope2[nt][e & 1], fabsf(static_cast<float>(rpos[nt][e & 1] - key)), v);
             }
-        }
       }
       if (kb + kKV4Keys > (p.causal ? min(len, pos0 + 1) : len)) {  // some key is hidden from some row
 #pragma unroll
@@ -678,7 +702,7 @@ __global__ void __launch_bounds__(kKV4Warps * 32, KV4Layout<D, NT>::kCtas)
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          mx[nt][e] = fmaxf(fmaxf(y[0][nt][e], y[0][nt][e + 2]), fmaxf(y[1][nt][e], y[1][nt][e + 2]));
+          mx[nt][e] = fmaxf(fmaxf(y[0][nt][e], y[0][nt][e + 2]), fmaxf(y[1][nt][e], y[1][nt][e + 2])) * fac[nt][e];
           up |= mx[nt][e] > m_run[nt][e] + 8.f;
         }
       if (__any_sync(0xffffffffu, up)) {
@@ -714,7 +738,7 @@ __global__ void __launch_bounds__(kKV4Warps * 32, KV4Layout<D, NT>::kCtas)
           float pr[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            pr[e] = ex2_approx(y[st][nt][e] - mu[nt][e & 1]);
+            pr[e] = ex2_approx(fmaf(y[st][nt][e], fac[nt][e & 1], -mu[nt][e & 1]));
             l_run[nt][e & 1] += pr[e];
           }
           pb[nt][0] = movmatrix_trans(pack_f16x2(pr[0], pr[1]));
@@ -728,7 +752,7 @@ __global__ void __launch_bounds__(kKV4Warps * 32, KV4Layout<D, NT>::kCtas)
           if constexpr (VW == 1) wv[e][0] = *src;
           else if constexpr (VW == 2) *reinterpret_cast<uint2 *>(wv[e]) = *reinterpret_cast<const uint2 *>(src);
           else *reinterpret_cast<uint4 *>(wv[e]) = *reinterpret_cast<const uint4 *>(src);
-          sm[e] = reinterpret_cast<const uint32_t *>(stage + L::kOffVP + key * (4 * G))[vgroup];
+          sm[e] = reinterpret_cast<const uint32_t *>(stage_par + (L::kOffVP - L::kOffKP) + key * (4 * G))[vgroup];
         }
         if (kb + kKV4Keys > len) {
           // rows behind the last key hold anything; 0 * NaN would spread
@@ -762,8 +786,9 @@ __global__ void __launch_bounds__(kKV4Warps * 32, KV4Layout<D, NT>::kCtas)
             }
           }
       }
+      }
       __syncwarp();  // every lane has read the stage
-      issue();
+      if (lane == 0) mbar_arrive(empty + 8 * st_);
     }
 
     // ---- the segment's end: join the warps (those without keys have m = -inf, l = 0, O = 0).
@@ -855,8 +880,8 @@ __global__ void __launch_bounds__(kKV4Warps * 32, KV4Layout<D, NT>::kCtas)
     cur.next(p);
   }
   // No copy may still be landing in shared memory when the CTA exits.
-  if (!ok && lane == 0)
-    for (int i = taken; i < issued; ++i) wait_drain(bars + 8 * (i % S), (i / S) & 1, 100000000ull);
+  if (*abort_flag != 0 && threadIdx.x == 0)
+    for (int i = max(0, misc[1] - S); i < misc[1]; ++i) wait_drain(full + 8 * (i % S), (i / S) & 1, 100000000ull);
 }
 
 // Joins the partial results of the segments that several pieces share (one warp per row):
