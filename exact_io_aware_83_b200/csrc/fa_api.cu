@@ -451,15 +451,15 @@ int kv4_row_tiles(int R, int d) { return R > 8 && d != 256 ? 2 : 1; }
 
 // Writes (store) or reads n tokens of the cache.
 int run_kv4_copy(bool store, fa::KV4Params &p, int d, cudaStream_t s) {
-  const long long threads = 2ll * p.B * p.Hkv * p.n * (d / 8);
-  const long long grid = (threads + 255) / 256;
-  if (grid >= (1ll << 31)) return FA_ERR_UNSUPPORTED;
-  const unsigned gr = static_cast<unsigned>(grid);
-  if (store) {
+  const long long rows = static_cast<long long>(p.B) * p.Hkv * p.n;  // below 2^31
+  if (store) {  // a thread per token and group of 32 channels, of K and of V
+    const unsigned gr = static_cast<unsigned>((2 * rows * (d / fa::kKV4Group) + 255) / 256);
     if (d == 64) fa::fa_kv4_write_kernel<64><<<gr, 256, 0, s>>>(p);
     else if (d == 128) fa::fa_kv4_write_kernel<128><<<gr, 256, 0, s>>>(p);
     else fa::fa_kv4_write_kernel<256><<<gr, 256, 0, s>>>(p);
-  } else {
+  } else {  // a thread per word of 8 channels of four tokens; K and V in y
+    const int per = 256 / (d / 8) * fa::kKV4ReadTokens;
+    const dim3 gr(static_cast<unsigned>((rows + per - 1) / per), 2);
     if (d == 64) fa::fa_kv4_read_kernel<64><<<gr, 256, 0, s>>>(p);
     else if (d == 128) fa::fa_kv4_read_kernel<128><<<gr, 256, 0, s>>>(p);
     else fa::fa_kv4_read_kernel<256><<<gr, 256, 0, s>>>(p);

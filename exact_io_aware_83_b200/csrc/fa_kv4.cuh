@@ -44,7 +44,7 @@ struct KV4Params {
   int B, Hkv, n, cap;
 };
 
-// One lane's eight bf16 values as fp32.
+// Eight bf16 values as fp32.
 __device__ __forceinline__ void unpack_bf16x8(const uint4 &w, float (&x)[8]) {
   const uint32_t u[4] = {w.x, w.y, w.z, w.w};
 #pragma unroll
@@ -71,27 +71,24 @@ __device__ __forceinline__ bool kv4_small_min(float m, float s) {
   return m != 0.f && fabsf(m) < s * 0.00390625f;
 }
 
-// Quantises the 32 values held by four lanes (8 each, lane c = lane % 4) and returns this
-// lane's word of codes, and s, m.
-__device__ __forceinline__ uint32_t kv4_quantise(float (&x)[8], __half &s_out, __half &m_out) {
-  float lo = x[0], hi = x[0], bad = 0.f;
+__device__ __forceinline__ __nv_bfloat162 u32_bf2(uint32_t u) { return *reinterpret_cast<__nv_bfloat162 *>(&u); }
+
+// Quantises a group of 32 bf16 values (16 words): four words of codes, and s, m.
+__device__ __forceinline__ void kv4_quantise(const uint32_t (&x)[16], uint32_t (&codes)[4], __half &s_out,
+                                             __half &m_out) {
+  __nv_bfloat162 l2 = u32_bf2(x[0]), h2 = l2;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    lo = fminf(lo, x[i]);
-    hi = fmaxf(hi, x[i]);
-    bad = fmaf(x[i], 0.f, bad);  // NaN as soon as a value is not finite
+  for (int i = 1; i < 16; ++i) {
+    l2 = __hmin2_nan(l2, u32_bf2(x[i]));
+    h2 = __hmax2_nan(h2, u32_bf2(x[i]));
   }
+  float lo = __bfloat162float(__hmin_nan(l2.x, l2.y)), hi = __bfloat162float(__hmax_nan(h2.x, h2.y));
 #pragma unroll
-  for (int o = 1; o < 4; o *= 2) {
-    lo = fminf(lo, __shfl_xor_sync(0xffffffffu, lo, o));
-    hi = fmaxf(hi, __shfl_xor_sync(0xffffffffu, hi, o));
-    bad += __shfl_xor_sync(0xffffffffu, bad, o);
-  }
-  if (bad != 0.f) {  // NaN
-    s_out = __ushort_as_half(0);
-    m_out = __ushort_as_half(0x7FFF);
-    return 0u;
-  }
+  for (int i = 0; i < 4; ++i) codes[i] = 0u;
+  s_out = __ushort_as_half(0);
+  m_out = __ushort_as_half(0x7FFF);
+  if (!(fabsf(lo) < INFINITY) || !(fabsf(hi) < INFINITY)) return;  // a NaN or an infinity
+  const bool clamp = lo < -kKV4Clamp || hi > kKV4Clamp;
   lo = fminf(fmaxf(lo, -kKV4Clamp), kKV4Clamp);
   hi = fminf(fmaxf(hi, -kKV4Clamp), kKV4Clamp);
   const __half mh = __float2half_rd(lo);
@@ -104,94 +101,126 @@ __device__ __forceinline__ uint32_t kv4_quantise(float (&x)[8], __half &s_out, _
     return kv4_small_min(m, t) ? fmaf(-15.f, t, hi) <= m : fmaf(15.f, t, m) >= hi;
   };
   const unsigned short sb1 = (sb > 0 && reaches(sb - 1)) ? sb - 1 : (reaches(sb) ? sb : sb + 1);
-  const __half sh = __ushort_as_half(sb1);
-  const float s = __half2float(sh);
-  s_out = sh;
+  s_out = __ushort_as_half(sb1);
   m_out = mh;
-  if (s == 0.f) return 0u;
+  const float s = __half2float(s_out);
+  if (s == 0.f) return;
   // t = (x - m) / s + 1/2 - 2^-8 in fp32 lies below the true quotient + 1/2 and above it
   // - 2^-7 (|m| / s <= 2^12, so rounding moves it by less than 2^-10), so its floor is n or
-  // n - 1; one exact comparison with the border above it decides.
-  const float inv = 1.f / s, c = fmaf(-m, inv, 0.5f - 0.00390625f);
+  // n - 1; one exact comparison with the border above it decides.  The floor: adding 2^23,
+  // rounded down, leaves it in the low bits.
+  const float inv = __fdividef(1.f, s), c = fmaf(-m, inv, 0.5f - 0.00390625f);
   const float mh2 = fmaf(0.5f, s, m);  // border above code 0
-  uint32_t word = 0;
   const bool small = kv4_small_min(m, s);
+  auto code = [&](float v, bool small_, bool clamp_) -> uint32_t {
+    if (clamp_) v = fminf(fmaxf(v, -kKV4Clamp), kKV4Clamp);
+    const float f = __fadd_rd(fmaf(v, inv, c), 8388608.f);
+    const float n0 = f - 8388608.f;
+    const bool above = small_ ? fmaf(-(n0 + 0.5f), s, v) >= m : v >= fmaf(n0, s, mh2);
+    return (__float_as_uint(f) & 15u) + (above ? 1u : 0u);
+  };
+  if (small || clamp) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const float v = fminf(fmaxf(x[i], -kKV4Clamp), kKV4Clamp);
-    const float n0 = floorf(fmaf(v, inv, c));
-    const bool above = small ? fmaf(-(n0 + 0.5f), s, v) >= m : v >= fmaf(n0, s, mh2);
-    const float n1 = above ? n0 + 1.f : n0;
-    word |= static_cast<uint32_t>(static_cast<int>(n1)) << (4 * i);
+    for (int i = 0; i < 16; ++i)
+      codes[i / 4] |= (code(__uint_as_float(x[i] << 16), small, clamp) |
+                       (code(__uint_as_float(x[i] & 0xFFFF0000u), small, clamp) << 4)) << (8 * (i % 4));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 16; ++i)
+      codes[i / 4] |= (code(__uint_as_float(x[i] << 16), false, false) |
+                       (code(__uint_as_float(x[i] & 0xFFFF0000u), false, false) << 4)) << (8 * (i % 4));
   }
-  return word;
 }
 
-// Writes new tokens: four lanes per (token, group), 8 channels a lane, K then V.  Bound:
-// HBM, 2 d bytes read and 5 d / 8 written per token for each of K and V.
+// Writes new tokens: a thread per (token, group), K's threads before V's.  Bound: HBM, 2 d
+// bytes read and 5 d / 8 written per token for each of K and V; a group per thread
+// spreads the search for s and m over 32 values and needs no exchange between lanes.
 template <int D>
 __global__ void __launch_bounds__(256) fa_kv4_write_kernel(const KV4Params p) {
-  constexpr int G = D / kKV4Group, T = D / 8;  // threads per token
-  const long long rows = static_cast<long long>(p.B) * p.Hkv * p.n;
-  const long long gid = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-  long long row = gid / T;
-  const int t = static_cast<int>(gid % T);  // word of the row: channels 8 t .. 8 t + 7
-  const bool is_v = row >= rows;
-  if (is_v) row -= rows;
-  const bool live = row < rows;  // whole groups of T >= 8 threads
-  int pos = -1;
-  long long bh = 0;
-  if (live) {
-    bh = row / p.n;
-    pos = kv4_position(p, static_cast<int>(bh / p.Hkv), static_cast<int>(row % p.n));
-  }
-  uint4 raw = make_uint4(0, 0, 0, 0);
-  if (pos >= 0) raw = *reinterpret_cast<const uint4 *>((is_v ? p.v : p.k) + row * D + t * 8);
-  float x[8];
-  unpack_bf16x8(raw, x);
-  __half s, m;
-  const uint32_t word = kv4_quantise(x, s, m);
-  if (pos < 0) return;
-  const int gamma = t / 4, c = t % 4;
-  const long long crow = bh * p.cap + pos;
-  const int place = is_v ? t : c * G + gamma;
-  reinterpret_cast<uint32_t *>((is_v ? p.vc : p.kc) + crow * (D / 2))[place] = word;
-  if (c == 0) {
-    __half *par = (is_v ? p.vp : p.kp) + crow * (2 * G);
-    par[is_v ? 2 * gamma : gamma] = s;
-    par[is_v ? 2 * gamma + 1 : G + gamma] = m;
-  }
-}
-
-// Reads n tokens back as bf16: value = bf16(m + n s), the sum exact in fp32.
-template <int D>
-__global__ void __launch_bounds__(256) fa_kv4_read_kernel(const KV4Params p) {
-  constexpr int G = D / kKV4Group, T = D / 8;
-  const long long rows = static_cast<long long>(p.B) * p.Hkv * p.n;
-  const long long gid = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
-  long long row = gid / T;
-  const int t = static_cast<int>(gid % T);
+  constexpr int G = D / kKV4Group;
+  const unsigned rows = static_cast<unsigned>(p.B) * p.Hkv * p.n;  // below 2^31
+  const unsigned long long gid = static_cast<unsigned long long>(blockIdx.x) * blockDim.x + threadIdx.x;
+  unsigned row = static_cast<unsigned>(gid / G);
+  const int gamma = static_cast<int>(gid % G);
   const bool is_v = row >= rows;
   if (is_v) row -= rows;
   if (row >= rows) return;
-  const long long bh = row / p.n;
-  const int pos = kv4_position(p, static_cast<int>(bh / p.Hkv), static_cast<int>(row % p.n));
+  const unsigned bh = row / static_cast<unsigned>(p.n);
+  const int pos = kv4_position(p, static_cast<int>(bh / static_cast<unsigned>(p.Hkv)),
+                               static_cast<int>(row - bh * static_cast<unsigned>(p.n)));
   if (pos < 0) return;
-  const int gamma = t / 4, c = t % 4;
-  const long long crow = bh * p.cap + pos;
-  const int place = is_v ? t : c * G + gamma;
-  const uint32_t word = reinterpret_cast<const uint32_t *>((is_v ? p.vc : p.kc) + crow * (D / 2))[place];
-  const __half *par = (is_v ? p.vp : p.kp) + crow * (2 * G);
-  const float s = __half2float(par[is_v ? 2 * gamma : gamma]);
-  const float m = __half2float(par[is_v ? 2 * gamma + 1 : G + gamma]);
-  uint32_t w[4];
+  uint32_t x[16];
+  const uint4 *src = reinterpret_cast<const uint4 *>((is_v ? p.v : p.k) + static_cast<size_t>(row) * D) + gamma * 4;
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float a = fmaf(static_cast<float>((word >> (8 * i)) & 15u), s, m);
-    const float b = fmaf(static_cast<float>((word >> (8 * i + 4)) & 15u), s, m);
-    w[i] = pack_bf16x2(a, b);
+  for (int i = 0; i < 4; ++i) *reinterpret_cast<uint4 *>(x + 4 * i) = __ldcs(src + i);
+  uint32_t codes[4];
+  __half s, m;
+  kv4_quantise(x, codes, s, m);
+  const size_t crow = static_cast<size_t>(bh) * p.cap + pos;
+  if (is_v) {
+    *reinterpret_cast<uint4 *>(p.vc + crow * (D / 2) + gamma * 16) = make_uint4(codes[0], codes[1], codes[2], codes[3]);
+    reinterpret_cast<__half2 *>(p.vp + crow * (2 * G))[gamma] = __halves2half2(s, m);
+  } else {
+    uint32_t *dst = reinterpret_cast<uint32_t *>(p.kc + crow * (D / 2));
+#pragma unroll
+    for (int c = 0; c < 4; ++c) dst[c * G + gamma] = codes[c];
+    p.kp[crow * (2 * G) + gamma] = s;
+    p.kp[crow * (2 * G) + G + gamma] = m;
   }
-  *reinterpret_cast<uint4 *>((is_v ? p.v : p.k) + row * D + t * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// Reads n tokens back as bf16: value = bf16(m + n s), the sum rounded once in fp32.  A thread
+// takes the same word of 8 channels of four tokens (blockDim / words apart), all their loads
+// before the first use.
+constexpr int kKV4ReadTokens = 4;
+
+template <int D>
+__global__ void __launch_bounds__(256) fa_kv4_read_kernel(const KV4Params p) {
+  constexpr int G = D / kKV4Group, T = D / 8, U = kKV4ReadTokens, P = 256 / T;
+  const unsigned rows = static_cast<unsigned>(p.B) * p.Hkv * p.n;
+  const int t = static_cast<int>(threadIdx.x % T), gamma = t / 4, c = t % 4;
+  const bool is_v = blockIdx.y != 0;
+  const uint8_t *codes = is_v ? p.vc : p.kc;
+  const __half *params = is_v ? p.vp : p.kp;
+  uint32_t word[U];
+  float s[U], m[U];
+  unsigned row[U];
+  bool live[U];
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    row[u] = (blockIdx.x * U + u) * P + threadIdx.x / T;
+    live[u] = row[u] < rows;
+    if (!live[u]) continue;
+    const unsigned bh = row[u] / static_cast<unsigned>(p.n);
+    const int pos = kv4_position(p, static_cast<int>(bh / static_cast<unsigned>(p.Hkv)),
+                                 static_cast<int>(row[u] - bh * static_cast<unsigned>(p.n)));
+    live[u] = pos >= 0;
+    if (!live[u]) continue;
+    const size_t crow = static_cast<size_t>(bh) * p.cap + pos;
+    word[u] = reinterpret_cast<const uint32_t *>(codes + crow * (D / 2))[is_v ? t : c * G + gamma];
+    const __half *par = params + crow * (2 * G);
+    if (is_v) {
+      const float2 sm = __half22float2(reinterpret_cast<const __half2 *>(par)[gamma]);
+      s[u] = sm.x;
+      m[u] = sm.y;
+    } else {
+      s[u] = __half2float(par[gamma]);
+      m[u] = __half2float(par[G + gamma]);
+    }
+  }
+#pragma unroll
+  for (int u = 0; u < U; ++u) {
+    if (!live[u]) continue;
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float a = fmaf(static_cast<float>((word[u] >> (8 * i)) & 15u), s[u], m[u]);
+      const float b = fmaf(static_cast<float>((word[u] >> (8 * i + 4)) & 15u), s[u], m[u]);
+      w[i] = pack_bf16x2(a, b);
+    }
+    __stcs(reinterpret_cast<uint4 *>((is_v ? p.v : p.k) + static_cast<size_t>(row[u]) * D + t * 8),
+           make_uint4(w[0], w[1], w[2], w[3]));
+  }
 }
 
 // ============================================================================ attention
