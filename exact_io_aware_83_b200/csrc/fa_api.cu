@@ -23,6 +23,7 @@
 #include "fa_bwd_pair.cuh"
 #include "fa_bwd_q128.cuh"
 #include "fa_decode.cuh"
+#include "fa_decode_score.cuh"
 #include "fa_kv4.cuh"
 
 namespace {
@@ -190,11 +191,9 @@ bool device_ready() {
     ok = ok && set_smem(fa_bwd_main_kernel<64, 64, 64, fa::kAttnScore>, BwdLayout<64, 64, 64>::kSmemBytesScore);
     ok = ok && set_smem(fa_bwd_main_kernel<128, 128, 64, fa::kAttnScore>, BwdLayout<128, 128, 64>::kSmemBytesScore);
     ok = ok && set_smem(fa_bwd_main_kernel<256, 128, 32, fa::kAttnScore>, BwdLayout<256, 128, 32>::kSmemBytesScore);
-    ok = ok && set_smem(fa::fa_decode_kernel<64, 16, true>, fa::DecodeLayout<64, 16>::kSmemBytes);
     ok = ok && set_smem(fa::fa_decode_kernel<64, 32, true>, fa::DecodeLayout<64, 32>::kSmemBytes);
     ok = ok && set_smem(fa::fa_decode_kernel<64, 64, true>, fa::DecodeLayout<64, 64>::kSmemBytes);
     ok = ok && set_smem(fa::fa_decode_kernel<64, 128, true>, fa::DecodeLayout<64, 128>::kSmemBytes);
-    ok = ok && set_smem(fa::fa_decode_kernel<128, 16, true>, fa::DecodeLayout<128, 16>::kSmemBytes);
     ok = ok && set_smem(fa::fa_decode_kernel<128, 32, true>, fa::DecodeLayout<128, 32>::kSmemBytes);
     ok = ok && set_smem(fa::fa_decode_kernel<128, 64, true>, fa::DecodeLayout<128, 64>::kSmemBytes);
     ok = ok && set_smem(fa::fa_decode_kernel<128, 128, true>, fa::DecodeLayout<128, 128>::kSmemBytes);
@@ -211,6 +210,11 @@ bool device_ready() {
     ok = ok && set_smem(fa::fa_decode_kv4_kernel<128, 2, true>, fa::KV4Layout<128, 2>::kSmemBytes);
     ok = ok && set_smem(fa::fa_decode_kv4_kernel<256, 1, false>, fa::KV4Layout<256, 1>::kSmemBytes);
     ok = ok && set_smem(fa::fa_decode_kv4_kernel<256, 1, true>, fa::KV4Layout<256, 1>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_score_kernel<64, 1>, fa::DecScoreLayout<64, 1>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_score_kernel<64, 2>, fa::DecScoreLayout<64, 2>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_score_kernel<128, 1>, fa::DecScoreLayout<128, 1>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_score_kernel<128, 2>, fa::DecScoreLayout<128, 2>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_score_kernel<256, 1>, fa::DecScoreLayout<256, 1>::kSmemBytes);
     using fa::FwdPLayout;
     ok = ok && set_smem(fa::fa_fwd_persist_kernel<64, fa::kAttnFull>, FwdPLayout<64>::kSmemBytes);
     ok = ok && set_smem(fa::fa_fwd_persist_kernel<64, fa::kAttnCausal>, FwdPLayout<64>::kSmemBytes);
@@ -403,8 +407,14 @@ template <int D, int RP>
 void launch_decode(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
                    const fa::DecodeParams &p, unsigned grid, bool score, cudaStream_t s) {
   constexpr int smem = fa::DecodeLayout<D, RP>::kSmemBytes;
-  if (score) fa::fa_decode_kernel<D, RP, true><<<grid, fa::kDecodeThreads, smem, s>>>(tq, tk, tv, p);
-  else fa::fa_decode_kernel<D, RP><<<grid, fa::kDecodeThreads, smem, s>>>(tq, tk, tv, p);
+  // (changed scores with up to 16 rows and d <= 128 have a kernel of their own)
+  if constexpr (RP > 16 || D == 256) {
+    if (score) {
+      fa::fa_decode_kernel<D, RP, true><<<grid, fa::kDecodeThreads, smem, s>>>(tq, tk, tv, p);
+      return;
+    }
+  }
+  fa::fa_decode_kernel<D, RP><<<grid, fa::kDecodeThreads, smem, s>>>(tq, tk, tv, p);
 }
 
 template <int D>
@@ -447,7 +457,7 @@ int check_kv4_decode(int B, int Hq, int Hkv, int Nq, int cap, int d, float scale
 }
 
 // 8-row tiles of query rows that one CTA takes together.
-int kv4_row_tiles(int R, int d) { return R > 8 && d != 256 ? 2 : 1; }
+int line_row_tiles(int R, int d) { return R > 8 && d != 256 ? 2 : 1; }
 
 // Writes (store) or reads n tokens of the cache.
 int run_kv4_copy(bool store, fa::KV4Params &p, int d, cudaStream_t s) {
@@ -467,8 +477,67 @@ int run_kv4_copy(bool store, fa::KV4Params &p, int d, cudaStream_t s) {
   return cuda_ok(cudaGetLastError(), store ? "fa_kv4_write launch" : "fa_kv4_read launch") ? FA_OK : FA_ERR_CUDA;
 }
 
-size_t kv4_workspace(int R, int d, int pieces) {
-  return pieces > 1 ? fa::pad256(static_cast<size_t>(pieces) * 2 * 8 * kv4_row_tiles(R, d) * (d + 2) * 4) : 0;
+// Scratch for the partial results of `pieces` pieces (fa_decode_line.cuh).
+size_t line_workspace(int R, int d, int pieces) {
+  return pieces > 1 ? fa::pad256(static_cast<size_t>(pieces) * 2 * 8 * line_row_tiles(R, d) * (d + 2) * 4) : 0;
+}
+
+// One piece per CTA that fits on the current device at once, but no more than there are blocks.
+int line_pieces(int B, int Hkv, int R, int cap, int d, int block, int ctas_per_sm) {
+  int sms = 148, dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) {
+    (void)cudaGetLastError();
+    sms = 148;
+  }
+  const int rows = 8 * line_row_tiles(R, d);
+  const long long slots = static_cast<long long>(sms) * ctas_per_sm;
+  const long long blocks = static_cast<long long>(B) * Hkv * ((R + rows - 1) / rows) * ((cap + block - 1) / block);
+  const long long s = blocks < slots ? blocks : slots;
+  return static_cast<int>(s < kMaxDecodeSplits ? s : kMaxDecodeSplits);
+}
+
+template <int D, int KB>
+void launch_line_merge_d(const fa::LineParams &p, int tile_rows, cudaStream_t s) {
+  const long long rows = static_cast<long long>(p.B) * p.Hkv * p.R;
+  fa::fa_line_merge_kernel<D, KB><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, s>>>(p, tile_rows);
+}
+
+// What a line of blocks needs besides the cache: sizes, lengths, scores, results.
+void fill_line(fa::LineParams &p, const void *q, void *o, float *lse, const int *lens, const float *slopes,
+               void *workspace, int B, int Hq, int Hkv, int Nq, int cap, int d, int causal, int pieces, float softcap,
+               float scale) {
+  p.q = static_cast<const __nv_bfloat16 *>(q);
+  p.lens = lens;
+  p.slopes = slopes;
+  p.o = static_cast<__nv_bfloat16 *>(o);
+  p.lse = lse;
+  p.part = static_cast<float *>(workspace);
+  p.B = B;
+  p.Hkv = Hkv;
+  p.Nq = Nq;
+  p.R = Hq / Hkv * Nq;
+  p.cap = cap;
+  const int tile_rows = 8 * line_row_tiles(p.R, d);
+  p.row_tiles = (p.R + tile_rows - 1) / tile_rows;
+  p.pieces = pieces;
+  p.causal = causal;
+  p.scale = scale;
+  p.sl2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
+  p.softcap = softcap;
+}
+
+// Decode with changed scores: rows per K/V head up to which the pieces of fa_decode_score.cuh
+// serve it.  Beyond, a second tile of rows would read the cache again, and the tcgen05 kernel,
+// which takes up to 128 rows at once, is used with its fixed key ranges.
+bool score_in_pieces(int R, int d) { return R <= (d == 256 ? 8 : 16); }
+constexpr int score_block(int d) { return d == 256 ? fa::DecScoreLayout<256, 1>::kBlock : fa::DecScoreLayout<128, 1>::kBlock; }
+
+template <int D, int NT>
+void launch_score_d(const CUtensorMap &tk, const CUtensorMap &tv, const fa::LineParams &p, cudaStream_t s) {
+  using L = fa::DecScoreLayout<D, NT>;
+  static_assert(L::kBlock == score_block(D), "block");
+  fa::fa_decode_score_kernel<D, NT><<<static_cast<unsigned>(p.pieces), L::W * 32, L::kSmemBytes, s>>>(tk, tv, p);
 }
 
 template <int D, int NT>
@@ -1175,14 +1244,64 @@ int fa_decode(const void *q, const void *k, const void *v, void *o, float *lse, 
                     scale, stream, nullptr);
 }
 
+int fa_decode_score_num_splits(int B, int Hq, int Hkv, int Nq, int Nk, int d) {
+  if (check_decode_sizes(B, Hq, Hkv, Nq, Nk, d, 1.0f) != FA_OK) return 0;
+  const int R = Hq / Hkv * Nq;
+  if (!score_in_pieces(R, d)) return fa_decode_num_splits(B, Hq, Hkv, Nq, Nk, d);
+  return line_pieces(B, Hkv, R, Nk, d, score_block(d), 1);
+}
+
+size_t fa_decode_score_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d, int num_splits) {
+  if (check_decode_sizes(B, Hq, Hkv, Nq, Nk, d, 1.0f) != FA_OK) return 0;
+  if (num_splits < 1 || num_splits > kMaxDecodeSplits) return 0;
+  const int R = Hq / Hkv * Nq;
+  return score_in_pieces(R, d) ? line_workspace(R, d, num_splits) : decode_workspace(B, Hq, Nq, d, num_splits);
+}
+
 int fa_decode_score(const void *q, const void *k, const void *v, void *o, float *lse, const int *seqlens_k,
                     const float *alibi_slopes, void *workspace, size_t workspace_bytes, int B, int Hq, int Hkv,
                     int Nq, int Nk, int d, int causal, int num_splits, float softcap, float scale, void *stream) {
-  const int rc = check_score_args(softcap, alibi_slopes);
+  if (!q || !k || !v || !o || !lse) return FA_ERR_INVALID_ARG;
+  if (causal != 0 && causal != 1) return FA_ERR_INVALID_ARG;
+  if (num_splits < 1 || num_splits > kMaxDecodeSplits) return FA_ERR_INVALID_ARG;
+  int rc = check_decode_sizes(B, Hq, Hkv, Nq, Nk, d, scale);
+  if (rc == FA_OK) rc = check_score_args(softcap, alibi_slopes);
   if (rc != FA_OK) return rc;
-  const fa::ScoreCfg score = make_score(softcap, alibi_slopes, nullptr, causal, scale);
-  return run_decode(q, k, v, o, lse, seqlens_k, workspace, workspace_bytes, B, Hq, Hkv, Nq, Nk, d, causal, num_splits,
-                    scale, stream, &score);
+  const int R = Hq / Hkv * Nq;
+  if (!score_in_pieces(R, d)) {
+    const fa::ScoreCfg score = make_score(softcap, alibi_slopes, nullptr, causal, scale);
+    return run_decode(q, k, v, o, lse, seqlens_k, workspace, workspace_bytes, B, Hq, Hkv, Nq, Nk, d, causal, num_splits,
+                      scale, stream, &score);
+  }
+  const size_t need = line_workspace(R, d, num_splits);
+  if (need > 0 && (!workspace || workspace_bytes < need)) return FA_ERR_WORKSPACE;
+  const void *ptrs[] = {q, k, v, o, lse};
+  for (const void *ptr : ptrs)
+    if (!aligned16(ptr)) return FA_ERR_ALIGN;
+  if ((need > 0 && !aligned16(workspace)) || (reinterpret_cast<uintptr_t>(seqlens_k) & 3u)) return FA_ERR_ALIGN;
+  if (!device_ready()) return FA_ERR_CUDA;
+  CUtensorMap tk, tv;
+  if (!make_map_bf16(&tk, k, d, Nk, static_cast<long long>(B) * Hkv, score_block(d)) ||
+      !make_map_bf16(&tv, v, d, Nk, static_cast<long long>(B) * Hkv, score_block(d))) {
+    if (debug_enabled()) std::fprintf(stderr, "[fa] cuTensorMapEncodeTiled failed (fa_decode_score)\n");
+    return FA_ERR_CUDA;
+  }
+  fa::LineParams p{};
+  fill_line(p, q, o, lse, seqlens_k, alibi_slopes, workspace, B, Hq, Hkv, Nq, Nk, d, causal, num_splits, softcap, scale);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool two = line_row_tiles(R, d) == 2;
+  const int tslot = timer_start(2, s);
+  if (d == 64) two ? launch_score_d<64, 2>(tk, tv, p, s) : launch_score_d<64, 1>(tk, tv, p, s);
+  else if (d == 128) two ? launch_score_d<128, 2>(tk, tv, p, s) : launch_score_d<128, 1>(tk, tv, p, s);
+  else launch_score_d<256, 1>(tk, tv, p, s);
+  timer_stop(2, tslot, s);
+  if (num_splits > 1 && Nk > score_block(d)) {  // segments of one block are never shared
+    const int tile_rows = two ? 16 : 8;
+    if (d == 64) launch_line_merge_d<64, score_block(64)>(p, tile_rows, s);
+    else if (d == 128) launch_line_merge_d<128, score_block(128)>(p, tile_rows, s);
+    else launch_line_merge_d<256, score_block(256)>(p, tile_rows, s);
+  }
+  return cuda_ok(cudaGetLastError(), "fa_decode_score launch") ? FA_OK : FA_ERR_CUDA;
 }
 
 int fa_kv4_write(const void *k, const void *v, void *k_codes, void *k_params, void *v_codes, void *v_params,
@@ -1242,26 +1361,15 @@ int fa_kv4_read(const void *k_codes, const void *k_params, const void *v_codes, 
 
 int fa_decode_kv4_num_splits(int B, int Hq, int Hkv, int Nq, int cap, int d) {
   if (check_kv4_decode(B, Hq, Hkv, Nq, cap, d, 1.0f) != FA_OK) return 0;
-  int sms = 148, dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess ||
-      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess || sms < 1) {
-    (void)cudaGetLastError();
-    sms = 148;
-  }
-  // One piece per CTA that fits on the device at once (two CTAs an SM up to 8 rows and d = 128),
-  // but no more than there are blocks of 256 keys.
-  const int R = Hq / Hkv * Nq, tiles = kv4_row_tiles(R, d), rows = 8 * tiles;
-  const long long slots = static_cast<long long>(sms) * (tiles == 1 && d <= 128 ? 2 : 1);
-  const long long blocks = static_cast<long long>(B) * Hkv * ((R + rows - 1) / rows) *
-                           ((cap + fa::kKV4Block - 1) / fa::kKV4Block);
-  const long long s = blocks < slots ? blocks : slots;
-  return static_cast<int>(s < kMaxDecodeSplits ? s : kMaxDecodeSplits);
+  const int R = Hq / Hkv * Nq;
+  // two CTAs an SM up to 8 rows and d = 128
+  return line_pieces(B, Hkv, R, cap, d, fa::kKV4Block, line_row_tiles(R, d) == 1 && d <= 128 ? 2 : 1);
 }
 
 size_t fa_decode_kv4_workspace_bytes(int B, int Hq, int Hkv, int Nq, int cap, int d, int num_splits) {
   if (check_kv4_decode(B, Hq, Hkv, Nq, cap, d, 1.0f) != FA_OK) return 0;
   if (num_splits < 1 || num_splits > kMaxDecodeSplits) return 0;
-  return kv4_workspace(Hq / Hkv * Nq, d, num_splits);
+  return line_workspace(Hq / Hkv * Nq, d, num_splits);
 }
 
 int fa_decode_kv4(const void *q, const void *k_codes, const void *k_params, const void *v_codes, const void *v_params,
@@ -1274,7 +1382,7 @@ int fa_decode_kv4(const void *q, const void *k_codes, const void *k_params, cons
   int rc = check_kv4_decode(B, Hq, Hkv, Nq, cap, d, scale);
   if (rc == FA_OK) rc = check_score_args(softcap, alibi_slopes);
   if (rc != FA_OK) return rc;
-  const size_t need = kv4_workspace(Hq / Hkv * Nq, d, num_splits);
+  const size_t need = line_workspace(Hq / Hkv * Nq, d, num_splits);
   if (need > 0 && (!workspace || workspace_bytes < need)) return FA_ERR_WORKSPACE;
   const void *ptrs[] = {q, k_codes, k_params, v_codes, v_params, o, lse};
   for (const void *ptr : ptrs)
@@ -1282,31 +1390,13 @@ int fa_decode_kv4(const void *q, const void *k_codes, const void *k_params, cons
   if ((need > 0 && !aligned16(workspace)) || (reinterpret_cast<uintptr_t>(seqlens_k) & 3u)) return FA_ERR_ALIGN;
   if (!device_ready()) return FA_ERR_CUDA;
 
-  const size_t rows = static_cast<size_t>(B) * Hq * Nq;
   fa::KV4DecodeParams p{};
-  p.q = static_cast<const __nv_bfloat16 *>(q);
+  fill_line(p, q, o, lse, seqlens_k, alibi_slopes, workspace, B, Hq, Hkv, Nq, cap, d, causal, num_splits, softcap, scale);
   p.kc = static_cast<const uint8_t *>(k_codes);
   p.vc = static_cast<const uint8_t *>(v_codes);
   p.kp = static_cast<const __half *>(k_params);
   p.vp = static_cast<const __half *>(v_params);
-  p.lens = seqlens_k;
-  p.slopes = alibi_slopes;
-  p.o = static_cast<__nv_bfloat16 *>(o);
-  p.lse = lse;
-  p.part = static_cast<float *>(workspace);
-  p.B = B;
-  p.Hkv = Hkv;
-  p.Nq = Nq;
-  p.R = Hq / Hkv * Nq;
-  p.cap = cap;
-  const bool two = kv4_row_tiles(p.R, d) == 2;
-  const int tile_rows = two ? 16 : 8;
-  p.row_tiles = (p.R + tile_rows - 1) / tile_rows;
-  p.pieces = num_splits;
-  p.causal = causal;
-  p.scale = scale;
-  p.sl2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-  p.softcap = softcap;
+  const bool two = line_row_tiles(p.R, d) == 2;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const int tslot = timer_start(2, s);
   if (d == 64) two ? launch_kv4<64, 2>(p, s) : launch_kv4<64, 1>(p, s);
@@ -1314,10 +1404,10 @@ int fa_decode_kv4(const void *q, const void *k_codes, const void *k_params, cons
   else launch_kv4<256, 1>(p, s);
   timer_stop(2, tslot, s);
   if (num_splits > 1 && cap > fa::kKV4Block) {  // segments of one block are never shared
-    const unsigned grid = static_cast<unsigned>((rows + 7) / 8);
-    if (d == 64) fa::fa_kv4_merge_kernel<64><<<grid, 256, 0, s>>>(p, tile_rows);
-    else if (d == 128) fa::fa_kv4_merge_kernel<128><<<grid, 256, 0, s>>>(p, tile_rows);
-    else fa::fa_kv4_merge_kernel<256><<<grid, 256, 0, s>>>(p, tile_rows);
+    const int tile_rows = two ? 16 : 8;
+    if (d == 64) launch_line_merge_d<64, fa::kKV4Block>(p, tile_rows, s);
+    else if (d == 128) launch_line_merge_d<128, fa::kKV4Block>(p, tile_rows, s);
+    else launch_line_merge_d<256, fa::kKV4Block>(p, tile_rows, s);
   }
   return cuda_ok(cudaGetLastError(), "fa_decode_kv4 launch") ? FA_OK : FA_ERR_CUDA;
 }

@@ -26,8 +26,7 @@
 #include <cuda_fp16.h>
 
 #include "fa_common.cuh"
-#include "fa_fwd.cuh"
-#include "fa_score.cuh"
+#include "fa_decode_line.cuh"
 
 namespace fa {
 
@@ -244,64 +243,18 @@ __global__ void __launch_bounds__(256) fa_kv4_read_kernel(const KV4Params p) {
 //    take without writing the widened values out and reading them back: 4 bytes a value
 //    through shared memory against half a byte from HBM.
 //  * Bound: HBM, 5 d / 4 bytes per key (K and V with their params).
-//  * Work: the valid tokens of every (batch entry, K/V head, row tile) - a segment - are cut
-//    into blocks of 256 keys, the blocks of all segments laid end to end and the line cut
-//    into `pieces` equal ranges, one CTA each, so that lengths that differ leave no SM idle.
-//    A segment that lies inside one piece is written by its CTA; one that several pieces
-//    share leaves a partial result per piece in the workspace, which fa_kv4_merge_kernel joins.
+//  * Work: blocks of 256 keys in equal pieces (fa_decode_line.cuh).
 //  * Blocks stream through a ring of shared-memory stages, across segments, four bulk copies
 //    each (the rows of one head are contiguous); every warp takes 32 keys of a block, and the
 //    warps take turns at refilling the stage that all have left.
-struct KV4DecodeParams {
-  const __nv_bfloat16 *q;  // [B, Hq, Nq, D]
+struct KV4DecodeParams : LineParams {
   const uint8_t *kc, *vc;
   const __half *kp, *vp;
-  const int *lens;         // [B] (nullptr: all `cap`), clamped to [0, cap]
-  const float *slopes;     // [Hq] or nullptr
-  __nv_bfloat16 *o;
-  float *lse;
-  float *part;             // [pieces][2][rows of a tile][D + 2] fp32 (O, then m and l)
-  int B, Hkv, Nq, R, cap;
-  int row_tiles, pieces;
-  int causal;
-  float scale, sl2;        // scale, scale * log2(e)
-  float softcap;           // 0: none
 };
 
 constexpr int kKV4Warps = 8;
 constexpr int kKV4Keys = 32;                        // keys per warp and step
 constexpr int kKV4Block = kKV4Warps * kKV4Keys;     // keys per block
-
-__device__ __forceinline__ int kv4_len(const KV4DecodeParams &p, int b) {
-  const int len = p.lens ? p.lens[b] : p.cap;
-  return len < 0 ? 0 : (len > p.cap ? p.cap : len);
-}
-// Blocks of a segment: one at least, so that a segment without keys is written too.
-__device__ __forceinline__ int kv4_blocks(int len) { return len > 0 ? (len + kKV4Block - 1) / kKV4Block : 1; }
-
-// Sum over the batch entries before `upto` of their blocks, times segments per entry (whole warp).
-__device__ __forceinline__ long long kv4_blocks_before(const KV4DecodeParams &p, int upto, int lane) {
-  long long n = 0;
-  for (int b = lane; b < upto; b += 32) n += kv4_blocks(kv4_len(p, b));
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) n += __shfl_xor_sync(0xffffffffu, n, o);
-  return n * (static_cast<long long>(p.Hkv) * p.row_tiles);
-}
-
-// First block of piece i of P over T blocks, and the piece that holds block x.
-__device__ __forceinline__ long long kv4_piece_begin(long long T, int P, int i) { return T * i / P; }
-__device__ __forceinline__ int kv4_piece_of(long long T, int P, long long x) {
-  return static_cast<int>(((x + 1) * P - 1) / T);
-}
-
-// The score in log2 units from x = scale q . k: capped, y = cap tanh(x / cap) log2(e).
-// tanh(u) = sign(u) (1 - w) / (1 + w), w = exp(-2 |u|): no cancellation that matters, the
-// absolute error stays below 2^-22 for every u.
-__device__ __forceinline__ float softcap_log2(float x, float inv_cap2, float cap_log2) {
-  // inv_cap2 = 2 log2(e) / cap
-  const float w = ex2_approx(-fabsf(x) * inv_cap2);
-  return copysignf(cap_log2 * __fdividef(1.f - w, 1.f + w), x);
-}
 
 __device__ __forceinline__ void mma_f16_16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
                                               uint32_t b0, uint32_t b1) {
@@ -319,12 +272,6 @@ __device__ __forceinline__ void mma_f16_16816_z(float (&d)[4], uint32_t a0, uint
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
 }
-__device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {
-  uint32_t r;
-  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(a));
-  return r;
-}
-
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   uint32_t r;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
@@ -388,25 +335,6 @@ __device__ __forceinline__ void bulk_load(uint32_t dst, const void *src, uint32_
                : "memory");
 }
 
-// A block of the line: its segment and its place in it.
-struct KV4Cursor {
-  int b, kvh, rt, blk, nblk, len;  // rt: row tile
-  __device__ __forceinline__ void enter(const KV4DecodeParams &p, int b_) {
-    b = b_;
-    len = kv4_len(p, b);
-    nblk = kv4_blocks(len);
-  }
-  __device__ __forceinline__ void next(const KV4DecodeParams &p) {
-    if (++blk < nblk) return;
-    blk = 0;
-    if (++rt < p.row_tiles) return;
-    rt = 0;
-    if (++kvh < p.Hkv) return;
-    kvh = 0;
-    if (b + 1 < p.B) enter(p, b + 1);
-  }
-};
-
 template <int D, int NT, bool CHANGED>  // CHANGED: capped scores or a distance bias
 __global__ void __launch_bounds__(kKV4Warps * 32, KV4Layout<D, NT>::kCtas)
     fa_decode_kv4_kernel(const KV4DecodeParams p) {
@@ -416,8 +344,9 @@ __global__ void __launch_bounds__(kKV4Warps * 32, KV4Layout<D, NT>::kCtas)
   const uint32_t base = (smem_u32(smem_raw) + 127u) & ~127u;
   uint8_t *smem = smem_raw + (base - smem_u32(smem_raw));
   float *sm_o = reinterpret_cast<float *>(smem + L::kOffPart);
-  float *sm_m = reinterpret_cast<float *>(smem + L::kOffM), *sm_l = sm_m + kKV4Warps * ROWS;
-  // [0] abort flag, [1] blocks whose copies have been started, [2..5] the piece, [6..11] what is loaded next
+  float *sm_m = reinterpret_cast<float *>(smem + L::kOffM);
+  // [0] abort flag, [1] blocks whose copies have been started, [2] blocks of the piece, [6..11]
+  // the block that is loaded next
   int *misc = reinterpret_cast<int *>(smem + L::kOffMisc);
 
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
@@ -432,64 +361,25 @@ __global__ void __launch_bounds__(kKV4Warps * 32, KV4Layout<D, NT>::kCtas)
     fence_mbar_init();
   }
   if (warp == 0) {
-    const long long per = static_cast<long long>(p.Hkv) * p.row_tiles;
-    long long T;
-    if (!p.lens) {
-      T = static_cast<long long>(p.B) * per * kv4_blocks(p.cap);
-    } else {
-      T = kv4_blocks_before(p, p.B, lane);
-    }
-    const long long x0 = kv4_piece_begin(T, p.pieces, blockIdx.x), x1 = kv4_piece_begin(T, p.pieces, blockIdx.x + 1);
-    // the batch entry that holds block x0: 32 entries at a time
-    long long before = 0;
-    int b = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-      const long long n = b0 + lane < p.B ? kv4_blocks(kv4_len(p, b0 + lane)) * per : 0;
-      long long sum = n;
-#pragma unroll
-      for (int o = 1; o < 32; o *= 2) {
-        const long long t = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o) sum += t;
-      }
-      const uint32_t hit = __ballot_sync(0xffffffffu, before + sum > x0 && n > 0);
-      if (hit) {
-        const int l = __ffs(hit) - 1;
-        b = b0 + l;
-        before += __shfl_sync(0xffffffffu, sum - n, l);
-        break;
-      }
-      before += __shfl_sync(0xffffffffu, sum, 31);
-    }
+    const LinePiece at = line_piece<kKV4Block>(p, blockIdx.x, lane);
     if (lane == 0) {
-      const int nblk = kv4_blocks(kv4_len(p, b));
-      const long long in = x0 - before;
       misc[0] = misc[1] = 0;
-      misc[2] = static_cast<int>(x1 - x0);
-      misc[3] = b;
-      misc[4] = static_cast<int>(in / nblk);
-      misc[5] = static_cast<int>(in % nblk);
-      KV4Cursor *ahead = reinterpret_cast<KV4Cursor *>(misc + 6);
-      ahead->enter(p, b);
-      ahead->kvh = misc[4] / p.row_tiles;
-      ahead->rt = misc[4] % p.row_tiles;
-      ahead->blk = misc[5];
+      misc[2] = at.blocks;
+      *reinterpret_cast<LineCursor<kKV4Block> *>(misc + 6) = line_cursor<kKV4Block>(p, at);
     }
   }
   __syncthreads();
   const int total = misc[2];  // blocks of the piece
   int todo = total, taken = 0;
-  KV4Cursor cur;              // what is computed next
-  cur.enter(p, misc[3]);
-  cur.kvh = misc[4] / p.row_tiles;
-  cur.rt = misc[4] % p.row_tiles;
-  cur.blk = misc[5];
+  LineCursor<kKV4Block> cur = *reinterpret_cast<LineCursor<kKV4Block> *>(misc + 6);  // what is computed next
+  __syncthreads();            // the cursor moves on with the first copies
   bool ok = true;
 
   // Starts the copies of the piece's next block (one thread; the cursor passes from one issuer
   // to the next through the barriers of the stage).
   auto issue = [&]() {
-    KV4Cursor *ahead = reinterpret_cast<KV4Cursor *>(misc + 6);
-    KV4Cursor a = *ahead;
+    LineCursor<kKV4Block> *ahead = reinterpret_cast<LineCursor<kKV4Block> *>(misc + 6);
+    LineCursor<kKV4Block> a = *ahead;
     const int st = misc[1] % S;
     const uint32_t dst = base + st * L::kStageBytes, bar = full + 8 * st;
     const int kb = a.blk * kKV4Block;
@@ -820,90 +710,20 @@ __global__ void __launch_bounds__(kKV4Warps * 32, KV4Layout<D, NT>::kCtas)
       if (lane == 0) mbar_arrive(empty + 8 * st_);
     }
 
-    // ---- the segment's end: join the warps (those without keys have m = -inf, l = 0, O = 0).
-    // Warps 4-7 hand their O, brought to the common maximum, to warps 0-3, which add their own;
-    // then every thread sums four of them.
-    __syncthreads();  // sm_* of the previous segment have been read
+    // Accumulator tile w * 4 + q of lane (g, c): channels 8 (g VW + w) + 2 q (+ 1), rows 2c, 2c+1.
+    line_join<D, NT, kKV4Warps>(p, sm_o, sm_m, m_run, l_run, r0, row0, began_before, ends_after, abort_flag,
+                                [&](float *row, float f, int nt, int e, bool add) {
+                                  float4 *dst = reinterpret_cast<float4 *>(row + 8 * g * VW);
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-#pragma unroll
-        for (int o = 4; o < 32; o *= 2) l_run[nt][e] += __shfl_xor_sync(0xffffffffu, l_run[nt][e], o);
-        if (g == 0) {
-          sm_m[warp * ROWS + nt * 8 + 2 * c + e] = m_run[nt][e];
-          sm_l[warp * ROWS + nt * 8 + 2 * c + e] = l_run[nt][e];
-        }
-      }
-    __syncthreads();
-    float scale_w[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float m = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kKV4Warps; ++w) m = fmaxf(m, sm_m[w * ROWS + nt * 8 + 2 * c + e]);
-        scale_w[nt][e] = ex2_approx(m_run[nt][e] - (m == -INFINITY ? 0.f : m));
-      }
-#pragma unroll
-    for (int turn = 0; turn < 2; ++turn) {
-      if (warp / 4 == 1 - turn) {
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const int r = nt * 8 + 2 * c + e;
-            if (r0 + r >= p.R) continue;
-            // Accumulator tile w * 4 + q of lane (g, c): channels 8 (g VW + w) + 2 q (+ 1), rows 2c, 2c+1.
-            float4 *dst = reinterpret_cast<float4 *>(sm_o + ((warp % 4) * ROWS + r) * D + 8 * g * VW);
-            const float f = scale_w[nt][e];
-#pragma unroll
-            for (int i = 0; i < MT; i += 2) {
-              float4 v = turn ? dst[i / 2] : make_float4(0.f, 0.f, 0.f, 0.f);
-              v.x = fmaf(f, acc[i][nt][e], v.x);
-              v.y = fmaf(f, acc[i][nt][e + 2], v.y);
-              v.z = fmaf(f, acc[i + 1][nt][e], v.z);
-              v.w = fmaf(f, acc[i + 1][nt][e + 2], v.w);
-              dst[i / 2] = v;
-            }
-          }
-      }
-      __syncthreads();
-    }
-    if (*abort_flag == 0) {
-      const bool direct = !began_before && !ends_after;
-      float *part = p.part + (static_cast<long long>(blockIdx.x) * 2 + (began_before ? 0 : 1)) * (ROWS * (D + 2));
-      for (int idx = threadIdx.x; idx < ROWS * (D / 2); idx += blockDim.x) {
-        const int r = idx / (D / 2), ch = 2 * (idx % (D / 2));
-        if (r0 + r >= p.R) break;
-        float m = -INFINITY;
-#pragma unroll
-        for (int w = 0; w < kKV4Warps; ++w) m = fmaxf(m, sm_m[w * ROWS + r]);
-        const float mu = m == -INFINITY ? 0.f : m;
-        float l = 0.f, o0 = 0.f, o1 = 0.f;
-#pragma unroll
-        for (int w = 0; w < kKV4Warps; ++w) l = fmaf(ex2_approx(sm_m[w * ROWS + r] - mu), sm_l[w * ROWS + r], l);
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const float2 o = *reinterpret_cast<const float2 *>(sm_o + (w * ROWS + r) * D + ch);
-          o0 += o.x;
-          o1 += o.y;
-        }
-        if (direct) {
-          const float inv = l == 0.f ? 0.f : 1.f / l;  // a row without keys: 0; NaN stays NaN
-          *reinterpret_cast<uint32_t *>(p.o + (row0 + r) * D + ch) = pack_bf16x2(o0 * inv, o1 * inv);
-          if (ch == 0) p.lse[row0 + r] = l == 0.f ? -INFINITY : (mu + log2f(l)) * kLn2;
-        } else {
-          float *dst = part + r * (D + 2);
-          *reinterpret_cast<float2 *>(dst + ch) = make_float2(o0, o1);
-          if (ch == 0) {
-            dst[D] = m;
-            dst[D + 1] = l;
-          }
-        }
-      }
-    }
+                                  for (int i = 0; i < MT; i += 2) {
+                                    float4 v = add ? dst[i / 2] : make_float4(0.f, 0.f, 0.f, 0.f);
+                                    v.x = fmaf(f, acc[i][nt][e], v.x);
+                                    v.y = fmaf(f, acc[i][nt][e + 2], v.y);
+                                    v.z = fmaf(f, acc[i + 1][nt][e], v.z);
+                                    v.w = fmaf(f, acc[i + 1][nt][e + 2], v.w);
+                                    dst[i / 2] = v;
+                                  }
+                                });
     todo -= count;
     cur.blk = cur.nblk - 1;  // to the next segment
     cur.next(p);
@@ -911,61 +731,6 @@ __global__ void __launch_bounds__(kKV4Warps * 32, KV4Layout<D, NT>::kCtas)
   // No copy may still be landing in shared memory when the CTA exits.
   if (*abort_flag != 0 && threadIdx.x == 0)
     for (int i = max(0, misc[1] - S); i < misc[1]; ++i) wait_drain(full + 8 * (i % S), (i / S) & 1, 100000000ull);
-}
-
-// Joins the partial results of the segments that several pieces share (one warp per row):
-// with the pieces' m_i (log2 units), l_i and unnormalised O_i,
-//   m = max m_i,  l = sum 2^(m_i - m) l_i,  O = sum 2^(m_i - m) O_i / l,  LSE = (m + log2 l) ln 2.
-template <int D>
-__global__ void __launch_bounds__(256) fa_kv4_merge_kernel(const KV4DecodeParams p, int tile_rows) {
-  constexpr int kPer = D / 32;
-  const int lane = threadIdx.x % 32;
-  const long long row = static_cast<long long>(blockIdx.x) * 8 + threadIdx.x / 32;
-  if (row >= static_cast<long long>(p.B) * p.Hkv * p.R) return;
-  const long long bh = row / p.R;
-  const int r = static_cast<int>(row % p.R), b = static_cast<int>(bh / p.Hkv), kvh = static_cast<int>(bh % p.Hkv);
-  const int nblk = kv4_blocks(kv4_len(p, b));
-  if (nblk == 1) return;  // one block is never shared
-  const long long per = static_cast<long long>(p.Hkv) * p.row_tiles;
-  const long long T = p.lens ? kv4_blocks_before(p, p.B, lane) : p.B * per * nblk;
-  const long long first = (p.lens ? kv4_blocks_before(p, b, lane) : b * per * nblk) +
-                          static_cast<long long>(kvh * p.row_tiles + r / tile_rows) * nblk;
-  const int p0 = kv4_piece_of(T, p.pieces, first), p1 = kv4_piece_of(T, p.pieces, first + nblk - 1);
-  if (p0 == p1) return;  // written by its piece
-  // The piece in which the segment begins holds it in slot 1 unless it begins with it too, in
-  // which case it began nowhere before: slot 1 as well.  Later pieces hold it in slot 0.
-  auto slot = [&](int i) {
-    return p.part + ((static_cast<long long>(i) * 2 + (i == p0 ? 1 : 0)) * tile_rows + r % tile_rows) * (D + 2);
-  };
-  // With fewer blocks than pieces some pieces are empty and hold nothing.
-  auto empty = [&](int i) { return kv4_piece_begin(T, p.pieces, i) == kv4_piece_begin(T, p.pieces, i + 1); };
-  float m = -INFINITY;
-  for (int i = p0 + lane; i <= p1; i += 32)
-    if (!empty(i)) m = fmaxf(m, slot(i)[D]);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  const float mu = m == -INFINITY ? 0.f : m;
-  float l = 0.f, acc[kPer];
-#pragma unroll
-  for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-#pragma unroll 4
-  for (int i = p0; i <= p1; ++i) {
-    if (T < p.pieces && empty(i)) continue;
-    const float *src = slot(i);
-    const float f = ex2_approx(src[D] - mu);
-    l = fmaf(f, src[D + 1], l);
-#pragma unroll
-    for (int e = 0; e < kPer; e += 2) {
-      const float2 o = *reinterpret_cast<const float2 *>(src + lane * kPer + e);
-      acc[e] = fmaf(f, o.x, acc[e]);
-      acc[e + 1] = fmaf(f, o.y, acc[e + 1]);
-    }
-  }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint32_t *dst = reinterpret_cast<uint32_t *>(p.o + row * D + lane * kPer);
-#pragma unroll
-  for (int e = 0; e < kPer; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-  if (lane == 0) p.lse[row] = l == 0.f ? -INFINITY : (mu + log2f(l)) * kLn2;
 }
 
 }  // namespace fa

@@ -127,6 +127,10 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
         lib.fa_decode_score.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, sz, ci, ci, ci, ci, ci, ci,
                                         ci, ci, cf, cf, vp]
         lib.fa_decode_score.restype = ci
+        lib.fa_decode_score_num_splits.argtypes = [ci, ci, ci, ci, ci, ci]
+        lib.fa_decode_score_num_splits.restype = ci
+        lib.fa_decode_score_workspace_bytes.argtypes = [ci, ci, ci, ci, ci, ci, ci]
+        lib.fa_decode_score_workspace_bytes.restype = sz
         lib.fa_kv4_write.argtypes = [vp, vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, vp]
         lib.fa_kv4_write.restype = ci
         lib.fa_kv4_read.argtypes = [vp, vp, vp, vp, vp, vp, vp, ci, ci, ci, ci, ci, vp]
@@ -292,6 +296,14 @@ def fa_bwd_score(q, k, v, o, lse, dout, dq, dk, dv, workspace, workspace_bytes, 
     _check(load().fa_bwd_score(q, k, v, o, lse, dout, dq, dk, dv, workspace, workspace_bytes,
                                alibi_slopes, key_range, B, Hq, Hkv, N, d, int(causal),
                                float(softcap), float(scale), stream), "fa_bwd_score")
+
+
+def fa_decode_score_num_splits(B, Hq, Hkv, Nq, Nk, d) -> int:
+    return int(load().fa_decode_score_num_splits(B, Hq, Hkv, Nq, Nk, d))
+
+
+def fa_decode_score_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, num_splits) -> int:
+    return int(load().fa_decode_score_workspace_bytes(B, Hq, Hkv, Nq, Nk, d, num_splits))
 
 
 def fa_decode_score(q, k, v, o, lse, seqlens_k, alibi_slopes, workspace, workspace_bytes, B, Hq,
@@ -472,6 +484,19 @@ def _out(t, name, shape, dtype, like):
     return t
 
 
+@functools.lru_cache(maxsize=1024)
+def _plan(which, device_index, B, Hq, Hkv, Nq, keys, d, num_splits):
+    """(splits, workspace bytes) of a decode with changed scores ("score") or over a 4-bit cache
+    ("kv4"): the sizes decide, on the current device."""
+    splits, nbytes = ((fa_decode_score_num_splits, fa_decode_score_workspace_bytes) if which == "score"
+                      else (fa_decode_kv4_num_splits, fa_decode_kv4_workspace_bytes))
+    if num_splits is None:
+        num_splits = splits(B, Hq, Hkv, Nq, keys, d)
+        if num_splits < 1:
+            raise FAError(FA_ERR_GQA if Hq % Hkv else FA_ERR_UNSUPPORTED, splits.__name__)
+    return num_splits, nbytes(B, Hq, Hkv, Nq, keys, d, num_splits)
+
+
 def _key_range(key_range, B, N, device):
     """Device pointer of the int32 [B, N, 2] key ranges (None stays None)."""
     import torch
@@ -615,6 +640,19 @@ def decode(q, k, v, seqlens_k=None, causal: bool = False, scale: float | None = 
             raise ValueError("seqlens_k must be a contiguous int32 CUDA tensor of B entries")
         lens_ptr = seqlens_k.data_ptr()
     scale = default_scale(d) if scale is None else scale
+    if _changes_scores(softcap, alibi_slopes):
+        _same_device(q, k, v, seqlens_k, workspace)
+        with _on(q.device):
+            num_splits, nbytes = _plan("score", q.device.index, B, Hq, Hkv, Nq, Nk, d, num_splits)
+            if workspace is None and nbytes > 0:
+                workspace = q.new_empty(nbytes, dtype=torch.uint8)
+            o = _out(out, "out", q.shape, torch.bfloat16, q)
+            l = _out(lse, "lse", (B, Hq, Nq), torch.float32, q)
+            fa_decode_score(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), l.data_ptr(), lens_ptr,
+                            _slopes(alibi_slopes, Hq, q.device), None if workspace is None else workspace.data_ptr(),
+                            0 if workspace is None else workspace.numel() * workspace.element_size(),
+                            B, Hq, Hkv, Nq, Nk, d, causal, num_splits, softcap, scale, _stream_handle(q))
+        return o, l
     if num_splits is None:
         num_splits = fa_decode_num_splits(B, Hq, Hkv, Nq, Nk, d)
         if num_splits < 1:
@@ -626,15 +664,6 @@ def decode(q, k, v, seqlens_k=None, causal: bool = False, scale: float | None = 
     l = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device) if lse is None else lse
     ws_ptr = None if workspace is None else workspace.data_ptr()
     ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    if _changes_scores(softcap, alibi_slopes):
-        _same_device(q, k, v, seqlens_k, workspace)
-        _out(o, "out", q.shape, torch.bfloat16, q)
-        _out(l, "lse", (B, Hq, Nq), torch.float32, q)
-        with _on(q.device):
-            fa_decode_score(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), l.data_ptr(), lens_ptr,
-                            _slopes(alibi_slopes, Hq, q.device), ws_ptr, ws_bytes, B, Hq, Hkv, Nq, Nk, d,
-                            causal, num_splits, softcap, scale, _stream_handle(q))
-        return o, l
     fa_decode(q.data_ptr(), k.data_ptr(), v.data_ptr(), o.data_ptr(), l.data_ptr(), lens_ptr,
               ws_ptr, ws_bytes, B, Hq, Hkv, Nq, Nk, d, causal, num_splits, scale,
               _stream_handle(q))
@@ -736,16 +765,6 @@ def kv4_read(cache, n: int, start=None, k=None, v=None):
     return k, v
 
 
-@functools.lru_cache(maxsize=1024)
-def _kv4_plan(device_index, B, Hq, Hkv, Nq, cap, d, num_splits):
-    """(splits, workspace bytes) of a decode_kv4 call; the sizes decide, on the current device."""
-    if num_splits is None:
-        num_splits = fa_decode_kv4_num_splits(B, Hq, Hkv, Nq, cap, d)
-        if num_splits < 1:
-            raise FAError(FA_ERR_GQA if Hq % Hkv else FA_ERR_UNSUPPORTED, "fa_decode_kv4_num_splits")
-    return num_splits, fa_decode_kv4_workspace_bytes(B, Hq, Hkv, Nq, cap, d, num_splits)
-
-
 def decode_kv4(q, cache, seqlens_k=None, causal: bool = False, scale: float | None = None,
                softcap: float = 0.0, alibi_slopes=None, num_splits: int | None = None, out=None,
                lse=None, workspace=None):
@@ -764,7 +783,7 @@ def decode_kv4(q, cache, seqlens_k=None, causal: bool = False, scale: float | No
     slopes_ptr = _slopes(alibi_slopes, Hq, q.device)
     scale = default_scale(d) if scale is None else scale
     with _on(q.device):
-        num_splits, nbytes = _kv4_plan(q.device.index, B, Hq, Hkv, Nq, cap, d, num_splits)
+        num_splits, nbytes = _plan("kv4", q.device.index, B, Hq, Hkv, Nq, cap, d, num_splits)
         if workspace is None and nbytes > 0:
             workspace = q.new_empty(nbytes, dtype=torch.uint8)
         o = _out(out, "out", q.shape, torch.bfloat16, q)

@@ -342,13 +342,23 @@ int fa_decode(const void *q, const void *k, const void *v, void *o, float *lse,
 
 /*
  * fa_decode with changed scores (softcap and alibi_slopes as for fa_fwd_score; the distance of
- * new row t and key j is |seqlens_k[b] - Nq + t - j|).  num_splits and workspace as for
- * fa_decode.  Rows of the cache behind the last valid key may hold anything.
+ * new row t and key j is |seqlens_k[b] - Nq + t - j|).  Rows of the cache behind the last
+ * valid key may hold anything.
+ *   num_splits: 1 .. 1024.  With up to 16 rows (Hq / Hkv) * Nq per K/V head (8 for d = 256),
+ *        the blocks of valid keys of all batch entries and heads are laid end to end and cut
+ *        into num_splits equal pieces, one CTA each, so that lengths that differ leave no SM
+ *        idle; with more rows, num_splits key ranges per head as in fa_decode.
+ *        fa_decode_score_num_splits gives the library's choice (0 for rejected sizes).
+ *   workspace: device scratch of fa_decode_score_workspace_bytes() bytes, 16-byte aligned (may
+ *        be NULL when that is 0, i.e. num_splits == 1).
  */
 int fa_decode_score(const void *q, const void *k, const void *v, void *o, float *lse,
                     const int *seqlens_k, const float *alibi_slopes, void *workspace,
                     size_t workspace_bytes, int B, int Hq, int Hkv, int Nq, int Nk, int d,
                     int causal, int num_splits, float softcap, float scale, void *stream);
+int fa_decode_score_num_splits(int B, int Hq, int Hkv, int Nq, int Nk, int d);
+size_t fa_decode_score_workspace_bytes(int B, int Hq, int Hkv, int Nq, int Nk, int d,
+                                       int num_splits);
 
 /*
  * The library's split count for fa_decode: enough (b, K/V head, key range) units to fill
