@@ -497,10 +497,27 @@ int line_pieces(int B, int Hkv, int R, int cap, int d, int block, int ctas_per_s
   return static_cast<int>(s < kMaxDecodeSplits ? s : kMaxDecodeSplits);
 }
 
+// The joining kernel, launched while the pieces are computed (it waits for them itself).
 template <int D, int KB>
-void launch_line_merge_d(const fa::LineParams &p, int tile_rows, cudaStream_t s) {
-  const long long rows = static_cast<long long>(p.B) * p.Hkv * p.R;
-  fa::fa_line_merge_kernel<D, KB><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, s>>>(p, tile_rows);
+bool launch_line_merge_d(const fa::LineParams &p, int tile_rows, cudaStream_t s) {
+  cudaLaunchAttribute early{};
+  early.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early.val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.Hkv * p.R);  // rows, below 2^31
+  cfg.blockDim = dim3(128);
+  cfg.stream = s;
+  cfg.attrs = &early;
+  cfg.numAttrs = 1;
+  return cuda_ok(cudaLaunchKernelEx(&cfg, fa::fa_line_merge_kernel<D, KB>, p, tile_rows), "fa_line_merge launch");
+}
+
+template <int KB64, int KB128, int KB256>
+bool launch_line_merge(const fa::LineParams &p, int d, cudaStream_t s) {
+  const int tile_rows = 8 * line_row_tiles(p.R, d);
+  if (d == 64) return launch_line_merge_d<64, KB64>(p, tile_rows, s);
+  if (d == 128) return launch_line_merge_d<128, KB128>(p, tile_rows, s);
+  return launch_line_merge_d<256, KB256>(p, tile_rows, s);
 }
 
 // What a line of blocks needs besides the cache: sizes, lengths, scores, results.
@@ -1295,13 +1312,10 @@ int fa_decode_score(const void *q, const void *k, const void *v, void *o, float 
   else if (d == 128) two ? launch_score_d<128, 2>(tk, tv, p, s) : launch_score_d<128, 1>(tk, tv, p, s);
   else launch_score_d<256, 1>(tk, tv, p, s);
   timer_stop(2, tslot, s);
-  if (num_splits > 1 && Nk > score_block(d)) {  // segments of one block are never shared
-    const int tile_rows = two ? 16 : 8;
-    if (d == 64) launch_line_merge_d<64, score_block(64)>(p, tile_rows, s);
-    else if (d == 128) launch_line_merge_d<128, score_block(128)>(p, tile_rows, s);
-    else launch_line_merge_d<256, score_block(256)>(p, tile_rows, s);
-  }
-  return cuda_ok(cudaGetLastError(), "fa_decode_score launch") ? FA_OK : FA_ERR_CUDA;
+  bool joined = true;
+  if (num_splits > 1 && Nk > score_block(d))  // segments of one block are never shared
+    joined = launch_line_merge<score_block(64), score_block(128), score_block(256)>(p, d, s);
+  return cuda_ok(cudaGetLastError(), "fa_decode_score launch") && joined ? FA_OK : FA_ERR_CUDA;
 }
 
 int fa_kv4_write(const void *k, const void *v, void *k_codes, void *k_params, void *v_codes, void *v_params,
@@ -1403,13 +1417,10 @@ int fa_decode_kv4(const void *q, const void *k_codes, const void *k_params, cons
   else if (d == 128) two ? launch_kv4<128, 2>(p, s) : launch_kv4<128, 1>(p, s);
   else launch_kv4<256, 1>(p, s);
   timer_stop(2, tslot, s);
-  if (num_splits > 1 && cap > fa::kKV4Block) {  // segments of one block are never shared
-    const int tile_rows = two ? 16 : 8;
-    if (d == 64) launch_line_merge_d<64, fa::kKV4Block>(p, tile_rows, s);
-    else if (d == 128) launch_line_merge_d<128, fa::kKV4Block>(p, tile_rows, s);
-    else launch_line_merge_d<256, fa::kKV4Block>(p, tile_rows, s);
-  }
-  return cuda_ok(cudaGetLastError(), "fa_decode_kv4 launch") ? FA_OK : FA_ERR_CUDA;
+  bool joined = true;
+  if (num_splits > 1 && cap > fa::kKV4Block)  // segments of one block are never shared
+    joined = launch_line_merge<fa::kKV4Block, fa::kKV4Block, fa::kKV4Block>(p, d, s);
+  return cuda_ok(cudaGetLastError(), "fa_decode_kv4 launch") && joined ? FA_OK : FA_ERR_CUDA;
 }
 
 int fa_merge(const float *o_parts, const float *lse_parts, void *o, float *lse, int num_parts, int rows,

@@ -48,11 +48,23 @@ __device__ __forceinline__ long long line_blocks_before(const LineParams &p, int
   return n * (static_cast<long long>(p.Hkv) * p.row_tiles);
 }
 
-// First block of piece i of P over T blocks, and the piece that holds block x.
-__device__ __forceinline__ long long line_piece_begin(long long T, int P, int i) { return T * i / P; }
-__device__ __forceinline__ int line_piece_of(long long T, int P, long long x) {
-  return static_cast<int>(((x + 1) * P - 1) / T);
+// First block of piece i of P over T blocks, and the piece that holds block x.  P <= T: with
+// fewer blocks than pieces the last CTAs have no work, so that no piece is empty.
+__device__ __forceinline__ int line_pieces_used(const LineParams &p, long long T) {
+  return T < p.pieces ? static_cast<int>(T) : p.pieces;
 }
+__device__ __forceinline__ long long line_div(long long a, long long b) {  // a, b >= 0; most fit 32 bits
+  return ((a | b) >> 32) == 0 ? static_cast<long long>(static_cast<uint32_t>(a) / static_cast<uint32_t>(b)) : a / b;
+}
+__device__ __forceinline__ long long line_piece_begin(long long T, int P, int i) { return line_div(T * i, P); }
+__device__ __forceinline__ int line_piece_of(long long T, int P, long long x) {
+  return static_cast<int>(line_div((x + 1) * P - 1, T));
+}
+
+// The kernel that follows in the stream may be launched (and wait) from here on; and: wait until
+// the kernel before this one has completed and its writes are visible.
+__device__ __forceinline__ void launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+__device__ __forceinline__ void wait_for_primary() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // The piece that CTA i works on: its number of blocks, and where the first one lies.
 struct LinePiece {
@@ -64,7 +76,9 @@ template <int KB>
 __device__ __forceinline__ LinePiece line_piece(const LineParams &p, int i, int lane) {
   const long long per = static_cast<long long>(p.Hkv) * p.row_tiles;
   const long long T = p.lens ? line_blocks_before<KB>(p, p.B, lane) : p.B * per * line_blocks<KB>(p.cap);
-  const long long x0 = line_piece_begin(T, p.pieces, i), x1 = line_piece_begin(T, p.pieces, i + 1);
+  const int P = line_pieces_used(p, T);
+  if (i >= P) return LinePiece{0, 0, 0, 0};
+  const long long x0 = line_piece_begin(T, P, i), x1 = line_piece_begin(T, P, i + 1);
   // the batch entry that holds block x0: 32 entries at a time
   long long before = 0;
   int b = 0;
@@ -87,7 +101,8 @@ __device__ __forceinline__ LinePiece line_piece(const LineParams &p, int i, int 
   }
   const int nblk = line_blocks<KB>(line_len(p, b));
   const long long in = x0 - before;
-  return LinePiece{static_cast<int>(x1 - x0), b, static_cast<int>(in / nblk), static_cast<int>(in % nblk)};
+  const int seg = static_cast<int>(line_div(in, nblk));
+  return LinePiece{static_cast<int>(x1 - x0), b, seg, static_cast<int>(in - static_cast<long long>(seg) * nblk)};
 }
 
 // A block of the line: its segment and its place in it.
@@ -221,35 +236,35 @@ __device__ __forceinline__ void line_join(const LineParams &p, float *sm_o, floa
   }
 }
 
-// Joins the partial results of the segments that several pieces share (one warp per row):
-// with the pieces' m_i (log2 units), l_i and unnormalised O_i,
+// Joins the partial results of the segments that several pieces share, one CTA of four warps
+// per row: with the pieces' m_i (log2 units), l_i and unnormalised O_i,
 //   m = max m_i,  l = sum 2^(m_i - m) l_i,  O = sum 2^(m_i - m) O_i / l,  LSE = (m + log2 l) ln 2.
+// Launched while the pieces are still being computed: it finds its pieces first, then waits.
+// (One warp per row, one piece after the other, took 11-15 us for 16 pieces a row.)
 template <int D, int KB>
-__global__ void __launch_bounds__(256) fa_line_merge_kernel(const LineParams p, int tile_rows) {
+__global__ void __launch_bounds__(128) fa_line_merge_kernel(const LineParams p, int tile_rows) {
   constexpr int kPer = D / 32;
-  const int lane = threadIdx.x % 32;
-  const long long row = static_cast<long long>(blockIdx.x) * 8 + threadIdx.x / 32;
-  if (row >= static_cast<long long>(p.B) * p.Hkv * p.R) return;
-  const long long bh = row / p.R;
-  const int r = static_cast<int>(row % p.R), b = static_cast<int>(bh / p.Hkv), kvh = static_cast<int>(bh % p.Hkv);
+  __shared__ float sm_acc[4][D], sm_l[4];
+  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  const long long row = blockIdx.x;
+  const int bh = static_cast<int>(blockIdx.x / static_cast<unsigned>(p.R)), r = static_cast<int>(blockIdx.x % static_cast<unsigned>(p.R));
+  const int b = bh / p.Hkv, kvh = bh % p.Hkv;
   const int nblk = line_blocks<KB>(line_len(p, b));
-  if (nblk == 1) return;  // one block is never shared
   const long long per = static_cast<long long>(p.Hkv) * p.row_tiles;
   const long long T = p.lens ? line_blocks_before<KB>(p, p.B, lane) : p.B * per * nblk;
   const long long first = (p.lens ? line_blocks_before<KB>(p, b, lane) : b * per * nblk) +
                           static_cast<long long>(kvh * p.row_tiles + r / tile_rows) * nblk;
-  const int p0 = line_piece_of(T, p.pieces, first), p1 = line_piece_of(T, p.pieces, first + nblk - 1);
+  const int P = line_pieces_used(p, T);
+  const int p0 = line_piece_of(T, P, first), p1 = line_piece_of(T, P, first + nblk - 1);
+  // Every CTA waits, so that what follows this kernel in the stream follows the pieces too.
+  wait_for_primary();
   if (p0 == p1) return;  // written by its piece
-  // The piece in which the segment begins holds it in slot 1 unless it begins with it too, in
-  // which case it began nowhere before: slot 1 as well.  Later pieces hold it in slot 0.
+  // The piece in which the segment begins holds it in slot 1, later ones in slot 0.
   auto slot = [&](int i) {
     return p.part + ((static_cast<long long>(i) * 2 + (i == p0 ? 1 : 0)) * tile_rows + r % tile_rows) * (D + 2);
   };
-  // With fewer blocks than pieces some pieces are empty and hold nothing.
-  auto empty = [&](int i) { return line_piece_begin(T, p.pieces, i) == line_piece_begin(T, p.pieces, i + 1); };
   float m = -INFINITY;
-  for (int i = p0 + lane; i <= p1; i += 32)
-    if (!empty(i)) m = fmaxf(m, slot(i)[D]);
+  for (int i = p0 + lane; i <= p1; i += 32) m = fmaxf(m, slot(i)[D]);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   const float mu = m == -INFINITY ? 0.f : m;
@@ -257,8 +272,7 @@ __global__ void __launch_bounds__(256) fa_line_merge_kernel(const LineParams p, 
 #pragma unroll
   for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
 #pragma unroll 4
-  for (int i = p0; i <= p1; ++i) {
-    if (T < p.pieces && empty(i)) continue;
+  for (int i = p0 + warp; i <= p1; i += 4) {
     const float *src = slot(i);
     const float f = ex2_approx(src[D] - mu);
     l = fmaf(f, src[D + 1], l);
@@ -269,11 +283,18 @@ __global__ void __launch_bounds__(256) fa_line_merge_kernel(const LineParams p, 
       acc[e + 1] = fmaf(f, o.y, acc[e + 1]);
     }
   }
-  const float inv = l == 0.f ? 0.f : 1.f / l;
-  uint32_t *dst = reinterpret_cast<uint32_t *>(p.o + row * D + lane * kPer);
 #pragma unroll
-  for (int e = 0; e < kPer; e += 2) dst[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-  if (lane == 0) p.lse[row] = l == 0.f ? -INFINITY : (mu + log2f(l)) * kLn2;
+  for (int e = 0; e < kPer; ++e) sm_acc[warp][lane * kPer + e] = acc[e];
+  if (lane == 0) sm_l[warp] = l;
+  __syncthreads();
+  l = (sm_l[0] + sm_l[1]) + (sm_l[2] + sm_l[3]);
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  for (int ch = 2 * threadIdx.x; ch < D; ch += 256) {
+    const float o0 = (sm_acc[0][ch] + sm_acc[1][ch]) + (sm_acc[2][ch] + sm_acc[3][ch]);
+    const float o1 = (sm_acc[0][ch + 1] + sm_acc[1][ch + 1]) + (sm_acc[2][ch + 1] + sm_acc[3][ch + 1]);
+    *reinterpret_cast<uint32_t *>(p.o + row * D + ch) = pack_bf16x2(o0 * inv, o1 * inv);
+  }
+  if (threadIdx.x == 0) p.lse[row] = l == 0.f ? -INFINITY : (mu + log2f(l)) * kLn2;
 }
 
 }  // namespace fa

@@ -94,6 +94,7 @@ __global__ void __launch_bounds__(DecScoreLayout<D, NT>::W * 32, 1)
     }
   }
   __syncthreads();
+  launch_dependents();        // the joining kernel
   const int total = misc[2];  // blocks of the piece
   int todo = total, taken = 0;
   LineCursor<KB> cur = *reinterpret_cast<LineCursor<KB> *>(misc + 6);  // what is computed next

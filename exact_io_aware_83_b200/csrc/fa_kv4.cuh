@@ -369,6 +369,7 @@ __global__ void __launch_bounds__(kKV4Warps * 32, KV4Layout<D, NT>::kCtas)
     }
   }
   __syncthreads();
+  launch_dependents();        // the joining kernel
   const int total = misc[2];  // blocks of the piece
   int todo = total, taken = 0;
   LineCursor<kKV4Block> cur = *reinterpret_cast<LineCursor<kKV4Block> *>(misc + 6);  // what is computed next
