@@ -98,15 +98,13 @@ __device__ __forceinline__ void score_tile_blocks(const int2 *span, int &first, 
   count = hi > 0 ? (hi - 1) / KB + 1 - first : 0;
 }
 
-// Hides with -inf the scores of keys kv0 + c outside [lo, hi); true when the warp had to.
+// Hides with -inf the scores of keys kv0 + c outside [lo, hi).
 template <int NC>
-__device__ __forceinline__ bool mask_score_range(uint32_t (&s)[NC], int lo, int hi, int kv0) {
+__device__ __forceinline__ void mask_score_range(uint32_t (&s)[NC], int lo, int hi, int kv0) {
   const int c_lo = lo - kv0, c_hi = hi - kv0;
-  if (!__any_sync(0xffffffffu, c_lo > 0 || c_hi < NC)) return false;
 #pragma unroll
   for (int c = 0; c < NC; ++c)
     if (c < c_lo || c >= c_hi) s[c] = __float_as_uint(-INFINITY);
-  return true;
 }
 
 // True when some key of the block [kv0, kv0 + KB) is hidden from some row of the
@@ -781,14 +779,24 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       }
       const int kv0 = (SPARSE ? (blist[cur] & 0x3FFF) : my_j0 + j) * 128;
       bool masked;
+      bool folded = false;  // changed scores: s holds raw products, rmax their largest
+      float rmax = 0.f;
       if constexpr (GEN) {
         masked = block_needs_mask<128>(p.left, p.right, sg.Lk, my_qb * 128 + sg.dlt, kv0);
         if (masked) mask_scores<128>(s, p.left, p.right, sg.Lk, qrow + sg.dlt, kv0);
       } else if constexpr (SCORE) {
-        const int side = kv0 + 127 <= my_qb * 128 ? -1 : (kv0 >= my_qb * 128 + 127 ? 1 : 0);
-        float none[1];
-        score_log2<128, false>(s, none, p.score, p.sl2, slope2, qrow, kv0, side);
-        masked = mask_score_range<128>(s, row_lo, row_hi, kv0);
+        const bool hides = __any_sync(0xffffffffu, row_lo > kv0 || row_hi < kv0 + 128);
+        if (p.score.raw_max > 0.f && !hides && !p.score.slopes) {
+          rmax = row_max<128>(s);
+          folded = __all_sync(0xffffffffu, fmaxf(rmax, -row_min<128>(s)) <= p.score.raw_max);
+        }
+        if (!folded) {
+          const int side = kv0 + 127 <= my_qb * 128 ? -1 : (kv0 >= my_qb * 128 + 127 ? 1 : 0);
+          float none[1];
+          score_log2<128, false>(s, none, p.score, p.sl2, slope2, qrow, kv0, side);
+          if (hides) mask_score_range<128>(s, row_lo, row_hi, kv0);
+        }
+        masked = hides;
       } else {
         const bool causal = MODE == kAttnCausal || (SPARSE && p.right == 0);
         masked = (causal && kv0 == my_qb * 128) || kv0 + 128 > p.N;
@@ -799,7 +807,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             if (kv0 + c >= lim) s[c] = __float_as_uint(-INFINITY);
         }
       }
-      const float smax = row_max128(s);
+      float smax;
+      if (SCORE && folded) smax = rmax * cap_poly(rmax, p.score);
+      else smax = row_max128(s);
       const float m_cand = smax * sl2;
       const float m_new = (m_cand > m_run + kRescaleThreshold) ? m_cand : m_run;
       // 0 on a row's first visible block, else <= 1.  A band or range can hide a whole block
@@ -807,13 +817,19 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
       const float alpha = (RANGED && m_new == m_run) ? 1.f : ex2_approx(m_run - m_new);
       const float m_use = (RANGED && m_new == -INFINITY) ? 0.f : m_new;
       float lsum, ppmax;
-      if (masked)
+      if (SCORE && folded) {
+        lsum = exp_block_capped<128>(s, p.score, m_new, tS);
+        ppmax = 0.f;
+      } else if (masked)
         exp_block<128, false, DROP>(s, sl2, m_use, tS, lsum, ppmax, p.drop, kv0 >> 3, qrow,
                                     b * p.Hq + my_h);   // exact zeros for masked keys
       else
         exp_block<128, true, DROP>(s, sl2, m_new, tS, lsum, ppmax, p.drop, kv0 >> 3, qrow, b * p.Hq + my_h);
       l_run = l_run * alpha + lsum;
-      r_run = r_run * alpha + (lsum + pmax_rounding(smax, sl2, m_use, ppmax));
+      if (SCORE && folded)
+        r_run = r_run * alpha + (lsum + pmax_rounding(rmax, cap_poly(rmax, p.score), m_use, ppmax));
+      else
+        r_run = r_run * alpha + (lsum + pmax_rounding(smax, sl2, m_use, ppmax));
       m_run = m_new;
       if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
         // O was last written by P V of block j-1.  Dense: it completed before S_j was

@@ -296,14 +296,24 @@ __global__ void __launch_bounds__(kFwdD256Threads, 1)
       tmem_ld_x64(tS, s);
       const int kv0 = (SPARSE ? blist[j] : jlo + j) * 64;
       bool masked;
+      bool folded = false;  // changed scores: s holds raw products, rmax their largest
+      float rmax = 0.f;
       if constexpr (GEN) {
         masked = block_needs_mask<64>(p.left, p.right, sg.Lk, qb * 128 + sg.dlt, kv0);
         if (masked) mask_scores<64>(s, p.left, p.right, sg.Lk, qrow + sg.dlt, kv0);
       } else if constexpr (SCORE) {
-        const int side = kv0 + 63 <= qb * 128 ? -1 : (kv0 >= qb * 128 + 127 ? 1 : 0);
-        float none[1];
-        score_log2<64, false>(s, none, p.score, p.sl2, slope2, qrow, kv0, side);
-        masked = mask_score_range<64>(s, row_lo, row_hi, kv0);
+        const bool hides = __any_sync(0xffffffffu, row_lo > kv0 || row_hi < kv0 + 64);
+        if (p.score.raw_max > 0.f && !hides && !p.score.slopes) {
+          rmax = row_max<64>(s);
+          folded = __all_sync(0xffffffffu, fmaxf(rmax, -row_min<64>(s)) <= p.score.raw_max);
+        }
+        if (!folded) {
+          const int side = kv0 + 63 <= qb * 128 ? -1 : (kv0 >= qb * 128 + 127 ? 1 : 0);
+          float none[1];
+          score_log2<64, false>(s, none, p.score, p.sl2, slope2, qrow, kv0, side);
+          if (hides) mask_score_range<64>(s, row_lo, row_hi, kv0);
+        }
+        masked = hides;
       } else {
         // (block-sparse: a row's first block always holds a visible key, the diagonal
         // block's first half coming before its second)
@@ -316,7 +326,9 @@ __global__ void __launch_bounds__(kFwdD256Threads, 1)
             if (kv0 + c >= lim) s[c] = __float_as_uint(-INFINITY);
         }
       }
-      const float smax = row_max<64>(s);
+      float smax;
+      if (SCORE && folded) smax = rmax * cap_poly(rmax, p.score);
+      else smax = row_max<64>(s);
       const float m_cand = smax * sl2;
       const float m_new = (m_cand > m_run + kRescaleThreshold) ? m_cand : m_run;
       // A band can hide a whole block from a row: while its max is still -inf the offset
@@ -324,12 +336,18 @@ __global__ void __launch_bounds__(kFwdD256Threads, 1)
       const float alpha = (RANGED && m_new == m_run) ? 1.f : ex2_approx(m_run - m_new);
       const float m_use = (RANGED && m_new == -INFINITY) ? 0.f : m_new;
       float lsum, ppmax;
-      if (masked)
+      if (SCORE && folded) {
+        lsum = exp_block_capped<64>(s, p.score, m_new, tS);
+        ppmax = 0.f;
+      } else if (masked)
         exp_block<64, false, DROP>(s, sl2, m_use, tS, lsum, ppmax, p.drop, kv0 >> 3, qrow, b * p.Hq + h);
       else
         exp_block<64, true, DROP>(s, sl2, m_new, tS, lsum, ppmax, p.drop, kv0 >> 3, qrow, b * p.Hq + h);
       l_run = l_run * alpha + lsum;
-      r_run = r_run * alpha + (lsum + pmax_rounding(smax, sl2, m_use, ppmax));
+      if (SCORE && folded)
+        r_run = r_run * alpha + (lsum + pmax_rounding(rmax, cap_poly(rmax, p.score), m_use, ppmax));
+      else
+        r_run = r_run * alpha + (lsum + pmax_rounding(smax, sl2, m_use, ppmax));
       m_run = m_new;
       if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
         // P V of block j-1 must have finished before O is rescaled.

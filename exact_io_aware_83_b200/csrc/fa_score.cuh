@@ -10,10 +10,13 @@
 // The gradient: with t = tanh(x / cap), d s_ij / d x = 1 - t^2; the bias is a constant.
 //
 // tanh.  MUFU.TANH is off by 2^-11 of its value: at cap = 50 a score of 20 would be off by
-// 0.01 and its probability by 1%.  Two forms take its place, chosen per warp and block by
-// the largest |x| / cap in it:
-//  * up to 0.7: t = u P(u^2), P of degree 4, this library's own minimax fit of the relative
-//    error of tanh(u) / u (3.1e-7), two scores per FMA-pipe instruction;
+// 0.01 and its probability by 1%.  Three forms take its place, chosen per warp and block by
+// the largest |u| = |x| / cap in it (all coefficients are this library's own minimax fits):
+//  * up to 0.5, in blocks without hidden keys and without a bias: t = u P(u^2), P of degree 3
+//    (relative error 5.4e-7), with scale, cap and log2(e) folded into the coefficients and the
+//    softmax's offset into the last product, so that a capped pair of scores costs five packed
+//    operations where a plain one costs one;
+//  * up to 0.7: the same with P of degree 4 (3.1e-7) in a pass of its own;
 //  * beyond: t = sign(u) (1 - w) / (1 + w), w = 2^(-2 log2(e) |u|): two MUFU operations; the
 //    absolute error stays below 2^-21, whatever u.  1 - t^2 is then 4 w / (1 + w)^2, which
 //    keeps its relative accuracy where t is near 1 (1 - t t would be all rounding there).
@@ -26,6 +29,8 @@ namespace fa {
 struct ScoreCfg {
   float cap_in;         // scale / cap (0: no cap)
   float cap_log2;       // cap * log2(e)
+  float raw_max;        // |q . k| up to which the folded polynomial holds (0: it is not used)
+  float c0, c1, c2, c3; // its coefficients: score in log2 units = r (c0 + c1 r^2 + c2 r^4 + c3 r^6), r = q . k
   const float *slopes;  // [Hq] or nullptr
   const int2 *range;    // [B, N] (lo, hi) or nullptr
   int causal;
@@ -53,6 +58,19 @@ __device__ __forceinline__ float tanh_any(float u, float &grad) {
   return copysignf((1.f - w) * r, u);
 }
 
+// P(r^2) of the folded polynomial for a pair of raw products r, |r| <= raw_max.
+__device__ __forceinline__ uint64_t f2_cap_poly(uint64_t r, const ScoreCfg &c) {
+  const uint64_t z = f2_mul(r, r);
+  uint64_t q = f2_fma(f2_pack(c.c3, c.c3), z, f2_pack(c.c2, c.c2));
+  q = f2_fma(q, z, f2_pack(c.c1, c.c1));
+  return f2_fma(q, z, f2_pack(c.c0, c.c0));
+}
+// The same for one product, operation by operation (so that the result has the same bits).
+__device__ __forceinline__ float cap_poly(float r, const ScoreCfg &c) {
+  const float z = r * r;
+  return fmaf(fmaf(fmaf(c.c3, z, c.c2), z, c.c1), z, c.c0);
+}
+
 // The visible keys of query row i (hi <= lo: none).
 __device__ __forceinline__ void row_range(const ScoreCfg &c, int b, int i, int N, int &lo, int &hi) {
   lo = 0;
@@ -67,6 +85,47 @@ __device__ __forceinline__ void row_range(const ScoreCfg &c, int b, int i, int N
     hi = min(r.y, N);
   }
   if (c.causal) hi = min(hi, i + 1);
+}
+
+// Smallest of N raw scores.
+template <int N>
+__device__ __forceinline__ float row_min(const uint32_t (&s)[N]) {
+  float m0 = INFINITY, m1 = INFINITY;
+#pragma unroll
+  for (int c = 0; c < N; c += 4) {
+    m0 = fmin3(m0, __uint_as_float(s[c + 0]), __uint_as_float(s[c + 1]));
+    m1 = fmin3(m1, __uint_as_float(s[c + 2]), __uint_as_float(s[c + 3]));
+  }
+  return fminf(m0, m1);
+}
+
+// P = 2^(score - m) of N raw products by the folded polynomial, packed to bf16 pairs and
+// stored to TMEM at tP, and their fp32 sum (the capped counterpart of exp_block).
+template <int N>
+__device__ __forceinline__ float exp_block_capped(const uint32_t (&s)[N], const ScoreCfg &cfg, float m, uint32_t tP) {
+  const uint64_t negm2 = f2_pack(-m, -m);
+  uint64_t l0 = 0, l1 = 0;  // packed (0.f, 0.f)
+#pragma unroll
+  for (int h = 0; h < N / 64; ++h) {
+    uint32_t pk[32];
+#pragma unroll
+    for (int q = 0; q < 32; ++q) {
+      const int pp = h * 32 + q;
+      const uint64_t r = f2_pack(__uint_as_float(s[2 * pp]), __uint_as_float(s[2 * pp + 1]));
+      float x0, x1;
+      f2_unpack(f2_fma(r, f2_cap_poly(r, cfg), negm2), x0, x1);
+      const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+      pk[q] = pack_bf16x2(p0, p1);
+      if (pp & 1)
+        l1 = f2_add(l1, f2_pack(p0, p1));
+      else
+        l0 = f2_add(l0, f2_pack(p0, p1));
+    }
+    tmem_st_x32(tP + h * 32, pk);
+  }
+  float a, b;
+  f2_unpack(f2_add(l0, l1), a, b);
+  return a + b;
 }
 
 // Largest |s| of N raw scores.

@@ -355,6 +355,13 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return r;
 }
 
+// min of three fp32 values in one instruction.
+__device__ __forceinline__ float fmin3(float a, float b, float c) {
+  float r;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+  return r;
+}
+
 // The two bf16 halves of a packed word, widened exactly to fp32.
 __device__ __forceinline__ uint64_t bf16x2_widen(uint32_t w) {
   return f2_pack(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
