@@ -315,15 +315,22 @@ fa::ScoreCfg make_score(float softcap, const float *slopes, const int *key_range
     c.cap_in = static_cast<float>(static_cast<double>(scale) / softcap);
     const double u = static_cast<double>(scale) / softcap, a = softcap * 1.4426950408889634;
     c.cap_log2 = static_cast<float>(a);
-    // tanh(u) / u on |u| <= 0.5 as a polynomial of u^2 (minimax fit, relative error 5.4e-7).
-    constexpr double k[4] = {0.9999994557708327, -0.33326317935183836, 0.13190296595162188, -0.044402225913669886};
-    if (u >= 0x1p-13 && u <= 0x1p10) {  // every folded coefficient is a normal fp32 number
-      c.raw_max = static_cast<float>(0.5 / u);
-      c.c0 = static_cast<float>(k[0] * a * u);
-      c.c1 = static_cast<float>(k[1] * a * u * u * u);
-      c.c2 = static_cast<float>(k[2] * a * u * u * u * u * u);
-      c.c3 = static_cast<float>(k[3] * a * u * u * u * u * u * u * u);
-    }
+    // tanh(u) / u as a polynomial of u^2: minimax fits on |u| <= 0.5 (degree 3, relative error
+    // 5.4e-7) and |u| <= 1 (degree 5, 5.9e-7), with a and the powers of scale / cap folded in;
+    // used where every coefficient is a normal fp32 number.
+    constexpr double t3[4] = {0.9999994557708327, -0.33326317935183836, 0.13190296595162188, -0.044402225913669886};
+    constexpr double t5[6] = {0.9999994135990478, -0.3332904237749518, 0.13281433872551196, -0.05160567377480486, 0.016743114805512608, -0.003067060223737072};
+    auto fold = [&](const double *t, int deg, float *k) {
+      bool normal = true;
+      double f = a * u;
+      for (int i = 0; i <= deg; ++i, f *= u * u) {
+        k[i] = static_cast<float>(t[i] * f);
+        normal = normal && std::fabs(t[i] * f) > 0x1p-120 && std::fabs(t[i] * f) < 0x1p120;
+      }
+      return normal;
+    };
+    if (fold(t3, 3, c.k3)) c.raw3 = static_cast<float>(0.5 / u);
+    if (fold(t5, 5, c.k5)) c.raw5 = static_cast<float>(1.0 / u);
   }
   c.slopes = slopes;
   c.range = reinterpret_cast<const int2 *>(key_range);

@@ -566,7 +566,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const uint32_t tS = tmem + L::kTmS + lane_off + c0;
     const uint32_t tDP = tmem + L::kTmDP + lane_off + c0;
     const bool row_live = kv < sg.Lk;
-    const float sl2 = SCORE ? 1.f : p.sl2;  // changed scores are in log2 units already
+    const float sl2 = p.sl2;
     bool ok = true;
     for (int i = 0; ok && i < T; ++i) {
       const int st = i % QS;
@@ -580,15 +580,38 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       const float4 *lse4 = reinterpret_cast<const float4 *>(vec + (st * 2) * BQ + c0);
       const float4 *dl4 = reinterpret_cast<const float4 *>(vec + (st * 2 + 1) * BQ + c0);
       float pr[HC];
-      float cgrad[SCORE ? HC : 1];  // changed scores: 1 - tanh^2
+      uint32_t spk[SCORE ? HC / 2 : 1];  // changed scores: P^T, while pr holds P (1 - tanh^2)
       {
         uint32_t rr[HC];
         if constexpr (HC == 32) tmem_ld_x32(tS, rr); else tmem_ld_x16(tS, rr);
         if constexpr (SCORE) {
           const float slope2 = p.score.slopes ? p.score.slopes[kvh * g + cur.hh] * kLog2e : 0.f;
           const int qa = q0 - c0, side = qa + BQ - 1 <= kv0 ? -1 : (qa >= kv0 + 127 ? 1 : 0);
-          score_log2<HC, true>(rr, cgrad, p.score, p.sl2, slope2, kv, q0, side);
-        }
+          const bool part = sc_flag[st] == 0;  // some row of the step does not see the whole key block
+          const int4 *lo4 = reinterpret_cast<const int4 *>(sc_range + (st * 2) * BQ + c0);
+          const int4 *hi4 = reinterpret_cast<const int4 *>(sc_range + (st * 2 + 1) * BQ + c0);
+          score_probs<HC>(rr, lse4, p.score, p.sl2, slope2, kv, q0, side,
+                          [&](int c, const float (&p4)[4], const float (&g4)[4]) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) pr[c + k] = g4[k];
+                            spk[c / 2] = pack_bf16x2(p4[0], p4[1]);
+                            spk[c / 2 + 1] = pack_bf16x2(p4[2], p4[3]);
+                          });
+          if (part || !row_live) {
+#pragma unroll
+            for (int c = 0; c < HC; c += 4) {
+              const int4 lo = lo4[c / 4], hi = hi4[c / 4];
+              const bool see[4] = {row_live && kv >= lo.x && kv < hi.x, row_live && kv >= lo.y && kv < hi.y,
+                                   row_live && kv >= lo.z && kv < hi.z, row_live && kv >= lo.w && kv < hi.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if (!see[k]) {
+                  pr[c + k] = 0.f;
+                  spk[(c + k) / 2] &= (k & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+                }
+            }
+          }
+        } else {
 #pragma unroll
         for (int c4 = 0; c4 < HC / 4; ++c4) {
           const float4 l = lse4[c4];
@@ -597,25 +620,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           pr[4 * c4 + 2] = ex2_approx(fmaf(__uint_as_float(rr[4 * c4 + 2]), sl2, -l.z));
           pr[4 * c4 + 3] = ex2_approx(fmaf(__uint_as_float(rr[4 * c4 + 3]), sl2, -l.w));
         }
+        }
       }
       // Masks: key rows past N, and queries q0 + c whose window misses this key
       // (visible iff c_lo <= c <= c_hi).  Query rows past N already have P = 0.
-      if (!row_live) {
+      if constexpr (SCORE) {
+        // done above
+      } else if (!row_live) {
 #pragma unroll
         for (int c = 0; c < HC; ++c) pr[c] = 0.f;
-      } else if constexpr (SCORE) {
-        if (!sc_flag[st]) {
-          const int4 *lo4 = reinterpret_cast<const int4 *>(sc_range + (st * 2) * BQ + c0);
-          const int4 *hi4 = reinterpret_cast<const int4 *>(sc_range + (st * 2 + 1) * BQ + c0);
-#pragma unroll
-          for (int c4 = 0; c4 < HC / 4; ++c4) {
-            const int4 lo = lo4[c4], hi = hi4[c4];
-            if (kv < lo.x || kv >= hi.x) pr[4 * c4 + 0] = 0.f;
-            if (kv < lo.y || kv >= hi.y) pr[4 * c4 + 1] = 0.f;
-            if (kv < lo.z || kv >= hi.z) pr[4 * c4 + 2] = 0.f;
-            if (kv < lo.w || kv >= hi.w) pr[4 * c4 + 3] = 0.f;
-          }
-        }
       } else if (GEN && (p.left >= 0 || p.right >= 0)) {
         const int c_lo = p.right < 0 ? INT_MIN : kv - p.right - sg.dlt - q0;
         const int c_hi = p.left < 0 ? INT_MAX : kv + p.left - sg.dlt - q0;
@@ -654,7 +667,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           }
         }
       }
-      {
+      if constexpr (SCORE) {
+        if constexpr (HC == 32) tmem_st_x16(tS, spk); else tmem_st_x8(tS, spk);
+      } else {
         // P^T as the A operand of dV += P^T dO: dropped entries are 0 (the 1 / (1 - p)
         // factor is applied to dV in the epilogue).
         uint32_t pk[HC / 2];
@@ -667,12 +682,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       tc_fence_before_sync();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::kBarP));
-      if constexpr (SCORE) {
-        if (p.score.cap_in > 0.f) {
-#pragma unroll
-          for (int c = 0; c < HC; ++c) pr[c] *= cgrad[c];  // dS = P (1 - tanh^2) (dP - Delta)
-        }
-      }
 
       if (!(ok = warp_wait_bounded(bar(L::kBarDP), i & 1, abort_flag, wait_site(3, L::kBarDP, i)))) break;
       tc_fence_after_sync();

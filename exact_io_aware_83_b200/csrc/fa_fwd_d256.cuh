@@ -277,7 +277,8 @@ __global__ void __launch_bounds__(kFwdD256Threads, 1)
     // l_run: sum of the fp32 probabilities (for the LSE); r_run: the same with each
     // block's largest probability counted as rounded to bf16 (see pmax_rounding).
     float m_run = -INFINITY, l_run = 0.f, r_run = 0.f;
-    const float sl2 = SCORE ? 1.f : p.sl2;  // changed scores are in log2 units already
+    const bool capped = SCORE && p.score.cap_in > 0.f, changed = capped || (SCORE && p.score.slopes);
+    const float sl2 = changed ? 1.f : p.sl2;  // changed scores are in log2 units already
     int row_lo = 0, row_hi = 0;
     float slope2 = 0.f;
     if constexpr (SCORE) {
@@ -296,21 +297,24 @@ __global__ void __launch_bounds__(kFwdD256Threads, 1)
       tmem_ld_x64(tS, s);
       const int kv0 = (SPARSE ? blist[j] : jlo + j) * 64;
       bool masked;
-      bool folded = false;  // changed scores: s holds raw products, rmax their largest
+      int folded = 0;  // changed scores: degree of the polynomial; s holds raw products, rmax their largest
       float rmax = 0.f;
       if constexpr (GEN) {
         masked = block_needs_mask<64>(p.left, p.right, sg.Lk, qb * 128 + sg.dlt, kv0);
         if (masked) mask_scores<64>(s, p.left, p.right, sg.Lk, qrow + sg.dlt, kv0);
       } else if constexpr (SCORE) {
         const bool hides = __any_sync(0xffffffffu, row_lo > kv0 || row_hi < kv0 + 64);
-        if (p.score.raw_max > 0.f && !hides && !p.score.slopes) {
+        if (capped && !hides && !p.score.slopes) {
           rmax = row_max<64>(s);
-          folded = __all_sync(0xffffffffu, fmaxf(rmax, -row_min<64>(s)) <= p.score.raw_max);
+          folded = cap_degree(fmaxf(rmax, -row_min<64>(s)), p.score);
         }
         if (!folded) {
-          const int side = kv0 + 63 <= qb * 128 ? -1 : (kv0 >= qb * 128 + 127 ? 1 : 0);
-          float none[1];
-          score_log2<64, false>(s, none, p.score, p.sl2, slope2, qrow, kv0, side);
+          // (ranges alone leave the scores as they are: sl2 goes into the exponent as usual)
+          if (changed) {
+            const int side = kv0 + 63 <= qb * 128 ? -1 : (kv0 >= qb * 128 + 127 ? 1 : 0);
+            float none[1];
+            score_log2<64, false>(s, none, p.score, p.sl2, slope2, qrow, kv0, side);
+          }
           if (hides) mask_score_range<64>(s, row_lo, row_hi, kv0);
         }
         masked = hides;
@@ -327,9 +331,9 @@ __global__ void __launch_bounds__(kFwdD256Threads, 1)
         }
       }
       float smax;
-      if (SCORE && folded) smax = rmax * cap_poly(rmax, p.score);
+      if (SCORE && folded) smax = rmax * cap_poly(folded, rmax, p.score);
       else smax = row_max<64>(s);
-      const float m_cand = smax * sl2;
+      const float m_cand = (SCORE && folded) ? smax : smax * sl2;
       const float m_new = (m_cand > m_run + kRescaleThreshold) ? m_cand : m_run;
       // A band can hide a whole block from a row: while its max is still -inf the offset
       // stays 0 and alpha 1.
@@ -337,7 +341,8 @@ __global__ void __launch_bounds__(kFwdD256Threads, 1)
       const float m_use = (RANGED && m_new == -INFINITY) ? 0.f : m_new;
       float lsum, ppmax;
       if (SCORE && folded) {
-        lsum = exp_block_capped<64>(s, p.score, m_new, tS);
+        if (folded == 3) lsum = exp_block_capped<64, 3>(s, p.score, m_new, tS);
+        else lsum = exp_block_capped<64, 5>(s, p.score, m_new, tS);
         ppmax = 0.f;
       } else if (masked)
         exp_block<64, false, DROP>(s, sl2, m_use, tS, lsum, ppmax, p.drop, kv0 >> 3, qrow, b * p.Hq + h);
@@ -345,7 +350,7 @@ __global__ void __launch_bounds__(kFwdD256Threads, 1)
         exp_block<64, true, DROP>(s, sl2, m_new, tS, lsum, ppmax, p.drop, kv0 >> 3, qrow, b * p.Hq + h);
       l_run = l_run * alpha + lsum;
       if (SCORE && folded)
-        r_run = r_run * alpha + (lsum + pmax_rounding(rmax, cap_poly(rmax, p.score), m_use, ppmax));
+        r_run = r_run * alpha + (lsum + pmax_rounding(rmax, cap_poly(folded, rmax, p.score), m_use, ppmax));
       else
         r_run = r_run * alpha + (lsum + pmax_rounding(smax, sl2, m_use, ppmax));
       m_run = m_new;
