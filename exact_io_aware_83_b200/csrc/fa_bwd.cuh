@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(256)
     *reinterpret_cast<float4 *>(qrow + c) = make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
-__global__ void __launch_bounds__(256)
+static __global__ void __launch_bounds__(256)
     fa_bwd_post_kernel(const float *__restrict__ dqacc, __nv_bfloat16 *__restrict__ dq, float scale,
                        long long n8) {
   const long long i = static_cast<long long>(blockIdx.x) * blockDim.x + threadIdx.x;
@@ -910,7 +910,8 @@ bool bwd_launch_pair(EncodeTiledFnBwd enc, const void *q, const void *k, const v
 // Dense d = 128 backward main kernel with 128-query steps (fa_bwd_q128.cuh), taken from
 // this sequence length on.
 constexpr int kQ128MinN = 4096;
-template <int MODE>
+constexpr float kGradUp = 1024.f;  // its dS with changed scores carries this factor (see there)
+template <int MODE, bool SCORE = false>
 bool bwd_launch_q128(EncodeTiledFnBwd enc, const void *q, const void *k, const void *v, const void *dout, void *dk,
                      void *dv, float *dqacc, int B, int Hq, int Hkv, int N, const BwdParams &p, cudaStream_t s);
 
@@ -919,7 +920,7 @@ inline int bwd_launch_d(const void *q, const void *k, const void *v, const void 
                         const void *dout, void *dq, void *dk, void *dv, void *workspace, int B, int Hq,
                         int Hkv, int N, int left, int right, float scale, cudaStream_t s, EncodeTiledFnBwd enc,
                         TimerStartFn tstart, TimerStopFn tstop, const PackedSeqs *pk, const DropCfg *drop,
-                        const uint8_t *bmask, BwdOrder order, const ScoreCfg *score) {
+                        const uint8_t *bmask, BwdOrder order) {
   const long long rows = pk ? static_cast<long long>(pk->total_q) * Hq : static_cast<long long>(B) * Hq * N;
   float *delta = static_cast<float *>(workspace);
   float *dqacc = reinterpret_cast<float *>(static_cast<char *>(workspace) + pad256(static_cast<size_t>(rows) * 4));
@@ -966,14 +967,6 @@ inline int bwd_launch_d(const void *q, const void *k, const void *v, const void 
   p.sl2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
   p.drop = drop ? *drop : DropCfg{};
   p.bmask = bmask;
-  p.score = score ? *score : ScoreCfg{};
-  p.blocks = nullptr;
-  if (score && score->range) {
-    // The spans of the query blocks, behind the dQ accumulator.
-    int2 *blocks = reinterpret_cast<int2 *>(static_cast<char *>(workspace) + bwd_workspace_bytes(B, Hq, N, D));
-    fa_score_blocks_kernel<<<dim3(static_cast<unsigned>(p.nkb), static_cast<unsigned>(B)), 128, 0, s>>>(*score, N, blocks);
-    p.blocks = blocks;
-  }
   // Unit order (unit_order): `order.tiers` tiers of key-block levels (1: head-major), the
   // last `order.tail` (b, kv head) rows level by level.
   const int tiers = order.tiers < 1 ? 1 : order.tiers;
@@ -986,7 +979,7 @@ inline int bwd_launch_d(const void *q, const void *k, const void *v, const void 
   // d = 256, and with 128-query steps at d = 128 from N = 4096 on.  Below that a CTA has
   // too few steps to repay the longer pipeline start of 128-query steps (measured on B200:
   // 128-query steps +4% at N = 8192, +2% at N = 4096, -5% at N = 2048).
-  const bool dense = !pk && !drop && !bmask && !score && left < 0 && right <= 0;
+  const bool dense = !pk && !drop && !bmask && left < 0 && right <= 0;
   if (dense && (D == 256 || (D == 128 && N >= kQ128MinN)) && grid > 0) {
     bool launched;
     if (D == 256)
@@ -1002,9 +995,7 @@ inline int bwd_launch_d(const void *q, const void *k, const void *v, const void 
   } else if (grid > 0) {
     // Dense full and causal attention have their own variants; packed sequences and other
     // bands take the general one.
-    if (score)
-      bwd_launch_main<D, DH, BQ, kAttnScore>(tq, tk, tv, tdo, tdk, tdv, tdq, p, grid, s);
-    else if (bmask)  // block-sparse: dense layout, causal or not (right = 0 or -1)
+    if (bmask)  // block-sparse: dense layout, causal or not (right = 0 or -1)
       bwd_launch_main<D, DH, BQ, kAttnSparse>(tq, tk, tv, tdo, tdk, tdv, tdq, p, grid, s);
     else if (drop && right == 0)  // dropout: dense attention only (the host checks)
       bwd_launch_main<D, DH, BQ, kAttnCausal, true>(tq, tk, tv, tdo, tdk, tdv, tdq, p, grid, s);
@@ -1030,17 +1021,16 @@ inline int bwd_launch(const void *q, const void *k, const void *v, const void *o
                       const void *dout, void *dq, void *dk, void *dv, void *workspace, int B, int Hq,
                       int Hkv, int N, int d, int left, int right, float scale, cudaStream_t s, Enc enc,
                       TimerStartFn tstart, TimerStopFn tstop, const PackedSeqs *pk = nullptr,
-                      const DropCfg *drop = nullptr, const uint8_t *bmask = nullptr, BwdOrder order = {1, 0},
-                      const ScoreCfg *score = nullptr) {
+                      const DropCfg *drop = nullptr, const uint8_t *bmask = nullptr, BwdOrder order = {1, 0}) {
   const EncodeTiledFnBwd e = reinterpret_cast<EncodeTiledFnBwd>(enc);
   if (d == 64)
     return bwd_launch_d<64, 64, 64>(q, k, v, o, lse, dout, dq, dk, dv, workspace, B, Hq, Hkv, N, left, right,
-                                    scale, s, e, tstart, tstop, pk, drop, bmask, order, score);
+                                    scale, s, e, tstart, tstop, pk, drop, bmask, order);
   if (d == 128)
     return bwd_launch_d<128, 128, 64>(q, k, v, o, lse, dout, dq, dk, dv, workspace, B, Hq, Hkv, N, left, right,
-                                      scale, s, e, tstart, tstop, pk, drop, bmask, order, score);
+                                      scale, s, e, tstart, tstop, pk, drop, bmask, order);
   return bwd_launch_d<256, 128, 32>(q, k, v, o, lse, dout, dq, dk, dv, workspace, B, Hq, Hkv, N, left, right,
-                                    scale, s, e, tstart, tstop, pk, drop, bmask, order, score);
+                                    scale, s, e, tstart, tstop, pk, drop, bmask, order);
 }
 
 }  // namespace fa

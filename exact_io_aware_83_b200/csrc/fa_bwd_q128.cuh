@@ -17,9 +17,17 @@
 // buffer for the drain's fp32 TMA reduce-adds of dQ.  The loader writes the next step's
 // Delta only after the elementwise warps have finished this step's dS^T.
 //
+// With SCORE the scores are capped or biased (fa_score.cuh; no key ranges): P and dS's factor
+// P (1 - tanh^2) are formed 32 query columns at a time.  The latter waits for dP^T as fp16 pairs,
+// times 2^10 (64 fp32 values a thread spill: 609 against 549 us at N = 4096 with 16 heads and two
+// entries): 11 significant bits from P = 6e-8 on, an eighth of the bf16 rounding that dS^T gets.
+// dS^T, dK and dQ carry the 2^10 until their last scaling.
+//
 // Roles: warps 0-7 P^T and dS^T (two warpgroups, 64 query columns each; thread = key
 // row), 8-11 the dQ drain (thread = d column), 12 the MMA issuer, 13 the loader.
 #pragma once
+
+#include <cuda_fp16.h>
 
 #include "fa_bwd.cuh"
 
@@ -69,7 +77,7 @@ struct Q128Layout {
   static_assert(kSmemBytes <= 232448, "shared-memory budget");
 };
 
-template <int MODE>
+template <int MODE, bool SCORE = false>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     fa_bwd_q128_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                        const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ CUtensorMap tm_do,
@@ -344,8 +352,35 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       // P = 0), then the bf16 pairs into the first 32 of its S^T columns.  The packed pairs
       // are also P for this step's dS: 64 fp32 values would leave too few of a thread's 128
       // registers to load dP^T in one piece.
-      uint32_t pk[HC / 2];
-      {
+      uint32_t pk[SCORE ? 1 : HC / 2];
+      uint32_t pg[SCORE ? HC / 2 : 1];  // changed scores: 2^10 P (1 - tanh^2), fp16 pairs
+      if constexpr (SCORE) {
+        const float slope2 = p.score.slopes ? p.score.slopes[step_head(i)] * kLog2e : 0.f;
+        const int qa = q0 - c0, side = qa + BQ - 1 <= kv0 ? -1 : (qa >= kv0 + 127 ? 1 : 0);
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+          uint32_t rr[32], pk32[16];
+          tmem_ld_x32(tS + 32 * h, rr);
+          score_probs<32>(rr, lse4 + 8 * h, p.score, sl2, slope2, kv, q0 + 32 * h, side,
+                          [&](int c, const float (&p4)[4], const float (&g4)[4]) {
+                            pg[16 * h + c / 2] = pack_f16x2(g4[0] * kGradUp, g4[1] * kGradUp);
+                            pg[16 * h + c / 2 + 1] = pack_f16x2(g4[2] * kGradUp, g4[3] * kGradUp);
+                            pk32[c / 2] = pack_bf16x2(p4[0], p4[1]);
+                            pk32[c / 2 + 1] = pack_bf16x2(p4[2], p4[3]);
+                          });
+          // keys past N and, causal, queries before this key
+          const int hidden = !row_live ? 32 : (MODE == kAttnCausal ? kv - q0 - 32 * h : 0);
+          if (hidden > 0) {
+#pragma unroll
+            for (int c = 0; c < 32; ++c)
+              if (c < hidden) {
+                pg[16 * h + c / 2] &= (c & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+                pk32[c / 2] &= (c & 1) ? 0x0000FFFFu : 0xFFFF0000u;
+              }
+          }
+          tmem_st_x16(tS + 16 * h, pk32);  // over columns that have been read
+        }
+      } else {
         uint32_t rr[HC];
         tmem_ld_x64(tS, rr);
         const bool diag = MODE == kAttnCausal && q0 < kv;
@@ -380,7 +415,23 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         break;
       if (!(ok = warp_wait_bounded(bar(L::kBarDP), i & 1, abort_flag, wait_site(kSite, L::kBarDP, i)))) break;
       tc_fence_after_sync();
-      {
+      if constexpr (SCORE) {
+        uint32_t rr[HC];
+        tmem_ld_x64(tDP, rr);
+#pragma unroll
+        for (int uu = 0; uu < HC / 8; ++uu) {
+          uint32_t w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int j = 4 * uu + e;
+            const float4 dd = dl4[j / 2];
+            const float d0 = (j & 1) ? dd.z : dd.x, d1 = (j & 1) ? dd.w : dd.y;
+            const float2 g2 = __half22float2(*reinterpret_cast<const __half2 *>(&pg[j]));
+            w[e] = pack_bf16x2(g2.x * (__uint_as_float(rr[2 * j]) - d0), g2.y * (__uint_as_float(rr[2 * j + 1]) - d1));
+          }
+          st_shared_v4(rowp + ((uu ^ (r & 7)) * 16), w[0], w[1], w[2], w[3]);
+        }
+      } else {
         uint32_t rr[HC];
         tmem_ld_x64(tDP, rr);
 #pragma unroll
@@ -411,7 +462,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     if (okw) {
       tc_fence_after_sync();
       const uint32_t tacc = tmem + (wg ? L::kTmDK : L::kTmDV) + lane_off;
-      const float mul = wg ? p.scale : 1.f;
+      const float mul = wg ? (SCORE ? p.scale / kGradUp : p.scale) : 1.f;
       const uint32_t stage = wg ? sK : sV;
 #pragma unroll
       for (int cc = 0; cc < 4; ++cc) {
@@ -497,7 +548,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   }
 }
 
-template <int MODE>
+template <int MODE, bool SCORE>
 inline bool bwd_launch_q128(EncodeTiledFnBwd enc, const void *q, const void *k, const void *v, const void *dout,
                             void *dk, void *dv, float *dqacc, int B, int Hq, int Hkv, int N, const BwdParams &p,
                             cudaStream_t s) {
@@ -511,7 +562,7 @@ inline bool bwd_launch_q128(EncodeTiledFnBwd enc, const void *q, const void *k, 
     return false;
   const unsigned grid = static_cast<unsigned>(B) * Hkv * p.nkb;
   if (grid == 0) return true;
-  fa_bwd_q128_kernel<MODE><<<grid, kBwdThreads, L::kSmemBytes, s>>>(tq, tk, tv, tdo, tdk, tdv, tdq, p);
+  fa_bwd_q128_kernel<MODE, SCORE><<<grid, kBwdThreads, L::kSmemBytes, s>>>(tq, tk, tv, tdo, tdk, tdv, tdq, p);
   return cudaGetLastError() == cudaSuccess;
 }
 

@@ -21,8 +21,8 @@ constexpr uint64_t kWaitLimitNs = 2000000000ull;
 
 // Device status word (FA_OK or FA_ERR_DEVICE_TIMEOUT) and the site of the first failure:
 // bits 0..15 iteration, 16..23 barrier id, 24..31 kernel id, 32..63 blockIdx.x.
-__device__ int g_fa_status;
-__device__ unsigned long long g_fa_status_site;
+static __device__ int g_fa_status;  // one per translation unit: fa_device_status looks at both
+static __device__ unsigned long long g_fa_status_site;
 
 __device__ __forceinline__ uint32_t wait_site(uint32_t kernel, uint32_t barrier, uint32_t iter) {
   return (kernel << 24) | ((barrier & 0xFFu) << 16) | (iter & 0xFFFFu);
@@ -173,7 +173,7 @@ __device__ __forceinline__ bool seq_geom(const int *cu_q, const int *cu_k, int N
 // Self-test of the watchdog path: one thread waits, with a short limit, on an mbarrier
 // that nothing ever arrives at.  The wait must give up, record FA_ERR_DEVICE_TIMEOUT in
 // the status word, and return; no fault, trap or hang is involved.
-__global__ void fa_watchdog_selftest_kernel(uint64_t limit_ns) {
+static __global__ void fa_watchdog_selftest_kernel(uint64_t limit_ns) {
   __shared__ __align__(8) uint64_t bar;
   __shared__ int abort_flag;
   if (threadIdx.x != 0) return;

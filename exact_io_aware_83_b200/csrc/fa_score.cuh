@@ -345,7 +345,7 @@ __device__ __forceinline__ void score_probs(uint32_t (&s)[N], const float4 *lse4
 
 // Smallest lo and largest hi over the rows of each 128-row query block that see a key
 // ((INT_MAX, 0) when none does): the backward's key blocks pick their query blocks by it.
-__global__ void __launch_bounds__(128) fa_score_blocks_kernel(const ScoreCfg cfg, int N, int2 *blocks) {
+static __global__ void __launch_bounds__(128) fa_score_blocks_kernel(const ScoreCfg cfg, int N, int2 *blocks) {
   __shared__ int red[2][4];
   const int qb = blockIdx.x, b = blockIdx.y;
   int lo, hi;

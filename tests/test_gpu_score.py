@@ -249,6 +249,42 @@ def test_long_row_against_a_slice():
         assert bool(((x - e).abs() <= 2.0 ** -8 * e.abs() + 2.0 ** -7.5 * s + 2.0 ** -18 * m + 2.0 ** -30).all())
 
 
+@pytest.mark.parametrize("kw", [dict(causal=True, softcap=50.0), dict(causal=False, softcap=3.0),
+                                dict(causal=True, alibi=True), dict(causal=True, softcap=8.0, alibi=True)])
+def test_long_rows_without_ranges(kw):
+    # from 4096 rows on, d = 128 without ranges takes 128-query steps; an odd length, grouped
+    # heads, small and large |score| / cap: one head and one group against the reference
+    N, d, scale = 4193, 128, 1 / math.sqrt(128)
+    q, k, v, do = _draw(1, 3, 1, N, d, seed=41, q_std=2.0)
+    slopes = _slopes(3) if kw.get("alibi") else None
+    gpu = dict(causal=kw["causal"], softcap=kw.get("softcap", 0.0), alibi_slopes=None if slopes is None else slopes.cuda())
+    qd, kd, vd, dod = (t.cuda() for t in (q, k, v, do))
+    o, lse = fa.fwd(qd, kd, vd, **gpu)
+    bufs, outs = zip(*(_guarded(t.shape, torch.bfloat16) for t in (q, k, v)))
+    fa.bwd(qd, kd, vd, o, lse, dod, dq=outs[0], dk=outs[1], dv=outs[2], **gpu)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status(None) == fa.FA_OK and _intact(*bufs)
+    args = dict(causal=kw["causal"], scale=scale, softcap=kw.get("softcap", 0.0), key_range=None)
+    want = [torch.zeros(t.shape, dtype=torch.float64) for t in (q, k, v)]
+    sums = [torch.zeros(t.shape, dtype=torch.float64) for t in (q, k, v)]
+    more = [torch.zeros(t.shape, dtype=torch.float64) for t in (q, k, v)]
+    for h in range(3):
+        hs = slice(h, h + 1)
+        one = [t.double() for t in (q[:, hs], k, v)]
+        sl = None if slopes is None else slopes[hs]
+        o_r, lse_r, av = ref.forward(*one, slopes=sl, **args)
+        got, l = o[:, hs].double().cpu(), lse[:, hs].double().cpu()
+        assert bool(((got - o_r).abs() <= 2.0 ** -8 * o_r.abs() + 2.0 ** -6.9 * av + 2.0 ** -30).all())
+        assert (l - lse_r).abs().max() <= 1e-4
+        for acc, part in zip((want, sums, more), ref.backward(*one, got, l, do[:, hs].double(), slopes=sl, **args)):
+            acc[0][:, hs] = part[0]
+            acc[1] += part[1]
+            acc[2] += part[2]
+    for x, e, s, m in zip(outs, want, sums, more):
+        x = x.double().cpu()
+        assert bool(((x - e).abs() <= 2.0 ** -8 * e.abs() + 2.0 ** -7.5 * s + 2.0 ** -18 * m + 2.0 ** -30).all())
+
+
 def test_captured_training_step():
     # forward and backward captured together and replayed on new inputs, against eager calls
     B, Hq, Hkv, N, d = 1, 4, 2, 300, 128
