@@ -15,6 +15,7 @@
 #include "fa_fwd.cuh"
 #include "fa_fwd_d256.cuh"
 #include "fa_bwd.cuh"
+#include "fa_bwd_plan.cuh"
 #include "fa_bwd_q128.cuh"
 #include "fa_decode.cuh"
 #include "fa_decode_score.cuh"
@@ -46,8 +47,11 @@ bool score_ready() {
     ok = ok && regs_at_least(fa::fa_fwd_kernel<128, fa::kAttnScore>, fa::kFwdRegsLaunch);
     ok = ok && set_smem(fa::fa_fwd_d256_kernel<fa::kAttnScore>, fa::FwdD256Layout::kSmemBytesScore);
     ok = ok && set_smem(fa::fa_bwd_main_kernel<64, 64, 64, fa::kAttnScore>, fa::BwdLayout<64, 64, 64>::kSmemBytesScore);
+    ok = ok && set_smem(fa::fa_bwd_main_kernel<64, 64, 64, fa::kAttnScoreParts>, fa::BwdLayout<64, 64, 64>::kSmemBytesScore);
     ok = ok && set_smem(fa::fa_bwd_main_kernel<128, 128, 64, fa::kAttnScore>, fa::BwdLayout<128, 128, 64>::kSmemBytesScore);
+    ok = ok && set_smem(fa::fa_bwd_main_kernel<128, 128, 64, fa::kAttnScoreParts>, fa::BwdLayout<128, 128, 64>::kSmemBytesScore);
     ok = ok && set_smem(fa::fa_bwd_main_kernel<256, 128, 32, fa::kAttnScore>, fa::BwdLayout<256, 128, 32>::kSmemBytesScore);
+    ok = ok && set_smem(fa::fa_bwd_main_kernel<256, 128, 32, fa::kAttnScoreParts>, fa::BwdLayout<256, 128, 32>::kSmemBytesScore);
     ok = ok && set_smem(fa::fa_decode_kernel<64, 32, true>, fa::DecodeLayout<64, 32>::kSmemBytes);
     ok = ok && set_smem(fa::fa_decode_kernel<64, 64, true>, fa::DecodeLayout<64, 64>::kSmemBytes);
     ok = ok && set_smem(fa::fa_decode_kernel<64, 128, true>, fa::DecodeLayout<64, 128>::kSmemBytes);
@@ -175,20 +179,36 @@ int launch_bwd_score(const BwdScoreArgs &a) {
   p.scale = a.scale;
   p.sl2 = static_cast<float>(static_cast<double>(a.scale) * 1.4426950408889634);
   p.score = a.score;
-  if (a.score.range) {
-    // The spans of the query blocks, behind the dQ accumulator.
-    int2 *blocks = reinterpret_cast<int2 *>(static_cast<char *>(a.workspace) + fa::bwd_workspace_bytes(a.B, a.Hq, a.N, D));
+  // Behind the dQ accumulator: the spans of the query blocks, then the plan.
+  char *behind = static_cast<char *>(a.workspace) + fa::bwd_workspace_bytes(a.B, a.Hq, a.N, D);
+  int2 *blocks = reinterpret_cast<int2 *>(behind);
+  const int max_parts = fa::plan_max_parts(a.B, a.Hkv, a.N, D);
+  const fa::PlanLayout plan = fa::plan_layout(a.B, a.Hkv, a.N, D, max_parts);
+  behind += fa::pad256(static_cast<size_t>(a.B) * p.nkb * 8);
+  int *parts = reinterpret_cast<int *>(behind + plan.parts);
+  if (max_parts > 0) {
+    int4 *items = reinterpret_cast<int4 *>(behind + plan.items);
+    fa::fa_bwd_plan_kernel<<<1, fa::kPlanThreads, 0, a.s>>>(a.score, a.B, a.N, p.nkb, a.Hq / a.Hkv, 128 / BQ,
+                                                          (a.N - (p.nkb - 1) * 128 + BQ - 1) / BQ, a.Hkv * (D / DH),
+                                                          max_parts, D == 256 ? 6 : 12, blocks, parts, items);
+    p.items = items;
+    p.parts = reinterpret_cast<float *>(behind + plan.sums);
+  } else if (a.score.range) {
     fa::fa_score_blocks_kernel<<<dim3(static_cast<unsigned>(p.nkb), static_cast<unsigned>(a.B)), 128, 0, a.s>>>(
         a.score, a.N, blocks);
-    p.blocks = blocks;
   }
+  if (a.score.range) p.blocks = blocks;
   const fa::BwdOrder order = bwd_order(a.B, a.Hkv, a.N, a.score.range ? a.N : -1, a.right);
   const int tiers = order.tiers < 1 ? 1 : order.tiers, heads = a.B * a.Hkv;
   p.tsz = (p.nkb + tiers - 1) / tiers;
   p.tail = order.tail < 0 ? 0 : (order.tail < heads ? order.tail : heads - 1);
 
-  // Without key ranges, d = 128 runs with 128-query steps from N = 4096 on, as plain scores do.
-  const bool wide = !a.score.range && D == 128 && a.N >= fa::kQ128MinN;
+  // With slopes, no key ranges and no plan, d = 128 runs with 128-query steps from N = 4096 on, as plain
+  // scores do: causal B = 2, Hq = 32, Hkv = 8, N = 4096 915 us against 978 with slopes, 1359
+  // against 1454 with both.  A cap alone fits the 64-query steps better as long as most scores
+  // stay in its shorter polynomials (1089 against 1055 us at cap 50 and standard normal q and k;
+  // 1152 against 1177 at cap 5).
+  const bool wide = a.score.slopes && !a.score.range && max_parts == 0 && D == 128 && a.N >= fa::kQ128MinN;
   bool launched = true;
   const int tslot = timer_start(1, a.s);
   if (wide) {
@@ -204,12 +224,23 @@ int launch_bwd_score(const BwdScoreArgs &a) {
                fa::bwd_map(e, &tk, a.k, false, D, a.N, hkv, 64, 128) && fa::bwd_map(e, &tv, a.v, false, D, a.N, hkv, 64, 128) &&
                fa::bwd_map(e, &tdk, a.dk, false, D, a.N, hkv, 64, 128) && fa::bwd_map(e, &tdv, a.dv, false, D, a.N, hkv, 64, 128) &&
                fa::bwd_map(e, &tdq, dqacc, true, D, a.N, hq, L::kDQCols, BQ);
-    const unsigned grid = static_cast<unsigned>(a.B) * a.Hkv * p.nkb * (D / DH);
-    if (launched) fa::bwd_launch_main<D, DH, BQ, fa::kAttnScore>(tq, tk, tv, tdo, tdk, tdv, tdq, p, grid, a.s);
+    const unsigned grid = static_cast<unsigned>(a.B) * a.Hkv * p.nkb * (D / DH) * (max_parts > 0 ? max_parts : 1);
+    if (launched && max_parts > 0)
+      fa::bwd_launch_main<D, DH, BQ, fa::kAttnScoreParts>(tq, tk, tv, tdo, tdk, tdv, tdq, p, grid, a.s);
+    else if (launched)
+      fa::bwd_launch_main<D, DH, BQ, fa::kAttnScore>(tq, tk, tv, tdo, tdk, tdv, tdq, p, grid, a.s);
   }
   timer_stop(1, tslot, a.s);
   if (!launched) return FA_ERR_CUDA;
   const long long n8 = rows * D / 8;
+  if (max_parts > 0) {
+    const long long ctas = (n8 + 255) / 256 + hkv * p.nkb * (D / 8);
+    fa::fa_bwd_join_kernel<D><<<static_cast<unsigned>(ctas), 256, 0, a.s>>>(
+        dqacc, static_cast<__nv_bfloat16 *>(a.dq), reinterpret_cast<const float4 *>(p.parts), parts,
+        static_cast<__nv_bfloat16 *>(a.dk), static_cast<__nv_bfloat16 *>(a.dv), a.scale, static_cast<int>(hkv), a.Hkv, a.N,
+        p.nkb, n8);
+    return cuda_ok(cudaGetLastError(), "fa_bwd_score launch") ? FA_OK : FA_ERR_CUDA;
+  }
   fa::fa_bwd_post_kernel<<<static_cast<unsigned>((n8 + 255) / 256), 256, 0, a.s>>>(
       dqacc, static_cast<__nv_bfloat16 *>(a.dq), wide ? a.scale / fa::kGradUp : a.scale, n8);
   return cuda_ok(cudaGetLastError(), "fa_bwd_score launch") ? FA_OK : FA_ERR_CUDA;
@@ -500,7 +531,8 @@ int fa_fwd_score(const void *q, const void *k, const void *v, void *o, float *ls
 
 size_t fa_bwd_score_workspace_bytes(int B, int Hq, int Hkv, int N, int d) {
   if (check_sizes(B, Hq, Hkv, N, d, 1.0f) != FA_OK) return 0;
-  return fa::bwd_workspace_bytes(B, Hq, N, d) + fa::pad256(static_cast<size_t>(B) * ((N + 127) / 128) * 8);
+  return fa::bwd_workspace_bytes(B, Hq, N, d) + fa::pad256(static_cast<size_t>(B) * ((N + 127) / 128) * 8) +
+         fa::pad256(fa::plan_layout(B, Hkv, N, d, fa::plan_max_parts(B, Hkv, N, d)).total);
 }
 
 int fa_bwd_score(const void *q, const void *k, const void *v, const void *o, const float *lse, const void *dout,

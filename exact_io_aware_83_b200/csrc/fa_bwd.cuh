@@ -114,8 +114,11 @@ struct BwdParams {
   const uint8_t *bmask;   // block-sparse: [B, Hq, nkb, nkb] 0/1 over 128 x 128 blocks
   int tsz;                // unit order: key-block levels per tier (see unit_order)
   int tail;               // unit order: heads taken level by level at the end
-  ScoreCfg score;         // changed scores (kAttnScore only)
+  ScoreCfg score;         // changed scores (kAttnScore, kAttnScoreParts only)
   const int2 *blocks;     // changed scores with key ranges: [B, nkb] span of each 128-row query block
+  const int4 *items;      // changed scores: (key block, batch entry, part, parts) in launch order
+                          //   (kAttnScoreParts only, see fa_bwd_plan.cuh)
+  float *parts;           // dK, dV of key blocks in several parts: [part][B, Hkv][nkb][dV | dK][D / 4][128][4] fp32
 };
 
 // D: head dimension (contraction of S^T and dP^T); DH: output columns owned by a CTA
@@ -242,6 +245,24 @@ struct SparseSteps {
       qb = -1;
     }
   }
+  // The next step becomes step number `step` of the walk, with the same `per_head` steps for
+  // every head.  (Only the last block can have fewer sub-blocks, and nothing follows it.)
+  __device__ __forceinline__ void seek(int step, int per_head) {
+    hh = step / per_head;
+    const int rem = step - hh * per_head;
+    int k = rem / nsub;
+    sub = rem - k * nsub - 1;
+    for (int w = 0; w < W; ++w) {
+      uint32_t u = bits[hh * stride + w];
+      const int c = __popc(u);
+      if (k < c) {
+        for (; k > 0; --k) u &= u - 1;
+        qb = w * 32 + __ffs(u) - 1;
+        return;
+      }
+      k -= c;
+    }
+  }
   template <int BQ>
   __device__ __forceinline__ int q0() const { return qb * 128 + sub * BQ; }
 };
@@ -278,7 +299,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   // mask) first
   const int half = static_cast<int>(blockIdx.x) % kHalves;
   int head, kb;
-  unit_order(static_cast<int>(blockIdx.x) / kHalves, p.B * p.Hkv, p.nkb, p.tsz, p.tail, head, kb);
+  constexpr bool SCORE = MODE == kAttnScore || MODE == kAttnScoreParts;
+  int part = 0, parts = 1;  // this CTA takes part `part` of `parts` of the unit's steps
+  if constexpr (MODE == kAttnScoreParts) {
+    const int u = static_cast<int>(blockIdx.x) / kHalves, item = u / p.Hkv;
+    const int4 it = p.items[item];
+    if (it.w == 0) return;  // behind the last part
+    kb = it.x;
+    head = it.y * p.Hkv + (u - item * p.Hkv);
+    part = it.z;
+    parts = it.w;
+  } else {
+    unit_order(static_cast<int>(blockIdx.x) / kHalves, p.B * p.Hkv, p.nkb, p.tsz, p.tail, head, kb);
+  }
   const int kvh = head % p.Hkv;
   const int b = head / p.Hkv;
   const int g = p.Hq / p.Hkv;
@@ -301,7 +334,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     q_first = MODE == kAttnCausal ? kv0 / BQ : 0;
     nq = (p.N + BQ - 1) / BQ - q_first;
   }
-  constexpr bool SCORE = MODE == kAttnScore;
   constexpr bool LISTED = MODE == kAttnSparse || SCORE;  // steps from a bitmap of query blocks
   constexpr bool SPARSE = MODE == kAttnSparse;
   constexpr bool GENLIKE = GEN || LISTED;  // a key block may see no query at all
@@ -408,6 +440,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   // Block-sparse: each role's cursor, moved once per step before (h, q0) are used.
   SparseSteps cur;
   if constexpr (LISTED) cur.init(spbits, spW, g, p.nkb, kSub, spSubLast, SCORE ? 0 : spW);
+  if constexpr (MODE == kAttnScoreParts) {
+    if (parts > 1) {
+      const int first = static_cast<int>(static_cast<long long>(T) * part / parts);
+      const int end = static_cast<int>(static_cast<long long>(T) * (part + 1) / parts);
+      if (end > first) cur.seek(first, T / g);
+      T = end - first;
+    }
+  }
 
   if (warp == 13) {
     // ================================================================ loader
@@ -742,6 +782,17 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0u;  // no query sees this block
         }
+        if constexpr (MODE == kAttnScoreParts) {
+          if (parts > 1) {  // summed, scaled and rounded by fa_bwd_join_kernel
+            // (four columns of all 128 rows next to one another: 512 bytes a warp and store)
+            uint4 *dst = reinterpret_cast<uint4 *>(p.parts) +
+                         ((((static_cast<size_t>(part) * p.B * p.Hkv + head) * p.nkb + kb) * 2 + wg) * (D / 4) +
+                          (dcol0 + cc * 32) / 4) * 128 + r;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) dst[e * 128] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            continue;
+          }
+        }
         const uint32_t rowbase = stage + (cc / 2) * L::kKChunk + r * 128;
 #pragma unroll
         for (int uu = 0; uu < 4; ++uu) {
@@ -757,7 +808,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             *reinterpret_cast<uint4 *>(drow + cc * 32 + uu * 8) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
-      if (!direct) {
+      if (!direct && !(MODE == kAttnScoreParts && parts > 1)) {
         fence_proxy_async_smem();
         named_bar_sync(1, 256);
         if (threadIdx.x == 0) {
@@ -889,7 +940,7 @@ inline void bwd_launch_main(const CUtensorMap &tq, const CUtensorMap &tk, const 
   using L = BwdLayout<D, DH, BQ>;
   fa_bwd_main_kernel<D, DH, BQ, MODE, DROP>
       <<<grid, kBwdThreads,
-         MODE == kAttnSparse ? L::kSmemBytesSparse : MODE == kAttnScore ? L::kSmemBytesScore : L::kSmemBytes, s>>>(tq, tk, tv, tdo, tdk,
+         MODE == kAttnSparse ? L::kSmemBytesSparse : MODE >= kAttnScore ? L::kSmemBytesScore : L::kSmemBytes, s>>>(tq, tk, tv, tdo, tdk,
                                                                                            tdv, tdq, p);
 }
 

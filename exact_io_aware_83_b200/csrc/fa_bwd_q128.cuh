@@ -19,8 +19,7 @@
 //
 // With SCORE the scores are capped or biased (fa_score.cuh; no key ranges): P and dS's factor
 // P (1 - tanh^2) are formed 32 query columns at a time.  The latter waits for dP^T as fp16 pairs,
-// times 2^10 (64 fp32 values a thread spill: 609 against 549 us at N = 4096 with 16 heads and two
-// entries): 11 significant bits from P = 6e-8 on, an eighth of the bf16 rounding that dS^T gets.
+// times 2^10 (64 fp32 values a thread spill): 11 significant bits from P = 6e-8 on, an eighth of the bf16 rounding that dS^T gets.
 // dS^T, dK and dQ carry the 2^10 until their last scaling.
 //
 // Roles: warps 0-7 P^T and dS^T (two warpgroups, 64 query columns each; thread = key

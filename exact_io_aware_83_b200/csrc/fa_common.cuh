@@ -110,8 +110,10 @@ struct DropCfg {
 // kAttnSparse: dense layout with a 0/1 mask over 128 x 128 blocks (and optionally the
 // causal mask); only enabled blocks are visited.
 // kAttnScore: dense layout with changed scores (a tanh cap, a distance bias, a key range per
-// query row; see fa_score.cuh).
-constexpr int kAttnFull = 0, kAttnCausal = 1, kAttnGeneral = 2, kAttnSparse = 3, kAttnScore = 4;
+// query row; see fa_score.cuh); kAttnScoreParts: the backward of it with the key blocks in
+// parts (fa_bwd_plan.cuh).
+constexpr int kAttnFull = 0, kAttnCausal = 1, kAttnGeneral = 2, kAttnSparse = 3, kAttnScore = 4,
+              kAttnScoreParts = 5;
 
 // Order of the work units of a grid: `heads` rows of `levels` units each, level 0 the
 // heaviest (the most key blocks under a causal mask).  Levels are cut into tiers of `tsz`

@@ -261,8 +261,9 @@ int fa_fwd_score(const void *q, const void *k, const void *v, void *o, float *ls
                  const float *alibi_slopes, const int *key_range, int B, int Hq, int Hkv, int N,
                  int d, int causal, float softcap, float scale, void *stream);
 
-/* Scratch bytes fa_bwd_score needs: those of fa_bwd and 8 bytes per batch entry and 128 query
- * rows, padded to 256.  0 for invalid sizes. */
+/* Scratch bytes fa_bwd_score needs: those of fa_bwd, 8 bytes per batch entry and 128 query
+ * rows and, where B * Hkv * ceil(N / 128) (twice that for d = 256) is below 148, a plan and fp32
+ * sums of dK and dV for each of up to 8 parts of the key blocks.  0 for invalid sizes. */
 size_t fa_bwd_score_workspace_bytes(int B, int Hq, int Hkv, int N, int d);
 
 /*

@@ -317,6 +317,42 @@ def _decode_ref(q, k, v, lens, causal, scale, softcap, slopes):
                                 softcap, None if slopes is None else slopes.double().numpy())
 
 
+def _mixed_ranges(B, N, seed):
+    # rows of every kind: none, one key, a stretch, all keys
+    g = torch.Generator().manual_seed(seed)
+    lo = torch.randint(0, N, (B, N), generator=g)
+    hi = lo + torch.randint(0, N, (B, N), generator=g)
+    kind = torch.randint(0, 4, (B, N), generator=g)
+    lo, hi = torch.where(kind == 3, 0, lo), torch.where(kind == 3, N, torch.where(kind == 2, lo + 1, hi))
+    return torch.stack((lo, torch.where(kind == 0, lo, hi)), -1).to(torch.int32)
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,N,d", [(2, 40, 40, 257, 64), (2, 40, 40, 257, 128), (2, 20, 20, 257, 256),
+                                          (49, 2, 1, 300, 64), (1, 6, 2, 1500, 128), (1, 8, 1, 1300, 64),
+                                          (1, 3, 1, 1100, 256)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_many_and_few_key_blocks(B, Hq, Hkv, N, d, causal):
+    # 240 units: whole key blocks; 147, 24, 11, 18: key blocks in parts
+    q, k, v, do = _draw(B, Hq, Hkv, N, d, seed=N + d + B)
+    check(q, k, v, do, causal=causal, softcap=30.0, slopes=_slopes(Hq), key_range=_mixed_ranges(B, N, N + Hq))
+
+
+@pytest.mark.parametrize("d", [64, 256])
+def test_parts_add_up_in_order(d):
+    # the same gradient of K and V every time; one key block with all the queries, the rest with few
+    B, Hq, Hkv, N = 1, 8, 1, 1200
+    q, k, v, do = (t.cuda() for t in _draw(B, Hq, Hkv, N, d, seed=5))
+    i = torch.arange(N, dtype=torch.int32, device="cuda")
+    rg = torch.stack((torch.zeros_like(i), torch.where(i < 1100, 100, N)), -1)[None].int().contiguous()
+    kw = dict(key_range=rg, alibi_slopes=_slopes(Hq).cuda())
+    o, lse = fa.fwd(q, k, v, **kw)
+    first = fa.bwd(q, k, v, o, lse, do, **kw)
+    for _ in range(3):
+        again = fa.bwd(q, k, v, o, lse, do, **kw)
+        assert torch.equal(again[1], first[1]) and torch.equal(again[2], first[2])
+    check(*(t.cpu() for t in (q, k, v, do)), slopes=_slopes(Hq), key_range=rg.cpu())
+
+
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("Hq,Hkv,Nq,Nk,lens,splits", [
     (4, 2, 1, 333, [333, 100], None), (8, 1, 1, 1000, [1000, 1], 3), (6, 2, 5, 700, [3, 700], 2),

@@ -67,9 +67,13 @@ def test_valid_arguments_without_a_device_report_cuda_error():
 
 def test_workspace_size():
     pad = lambda x: (x + 255) // 256 * 256
-    for B, Hq, N, d in ((1, 2, 100, 64), (3, 4, 5000, 128)):
-        assert fa.fa_bwd_score_workspace_bytes(B, Hq, 1, N, d) == \
-            fa.fa_bwd_workspace_bytes(B, Hq, 1, N, d) + pad(B * ((N + 127) // 128) * 8)
+    # spans; with less than 148 units part counts, items, and fp32 dK and dV of every part
+    for B, Hq, Hkv, N, d, parts in ((1, 2, 1, 100, 64, 8), (3, 4, 1, 5000, 128, 4), (2, 8, 8, 4096, 256, 0),
+                                    (1, 8, 4, 2048, 256, 4), (1, 4, 4, 4736, 128, 0), (1, 3, 3, 6272, 128, 4)):
+        blocks = B * ((N + 127) // 128)
+        plan = pad(4 * blocks) + pad(16 * parts * blocks) + parts * Hkv * 128 * blocks * d * 8 if parts else 0
+        assert fa.fa_bwd_score_workspace_bytes(B, Hq, Hkv, N, d) == \
+            fa.fa_bwd_workspace_bytes(B, Hq, Hkv, N, d) + pad(8 * blocks) + pad(plan)
     assert fa.fa_bwd_score_workspace_bytes(1, 4, 3, 100, 64) == 0
 
 
