@@ -794,7 +794,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if (!folded) {
           // (ranges alone leave the scores as they are: sl2 goes into the exponent as usual)
           if (changed) {
-            const int side = kv0 + 127 <= my_qb * 128 ? -1 : (kv0 >= my_qb * 128 + 127 ? 1 : 0);
+            const int side = p.score.causal || kv0 + 127 <= my_qb * 128 ? -1 : (kv0 >= my_qb * 128 + 127 ? 1 : 0);
             float none[1];
             score_log2<128, false>(s, none, p.score, p.sl2, slope2, qrow, kv0, side);
           }

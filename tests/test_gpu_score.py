@@ -337,6 +337,14 @@ def test_many_and_few_key_blocks(B, Hq, Hkv, N, d, causal):
     check(q, k, v, do, causal=causal, softcap=30.0, slopes=_slopes(Hq), key_range=_mixed_ranges(B, N, N + Hq))
 
 
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("softcap,q_std", [(50.0, 1.0), (8.0, 2.0), (1.0, 4.0)])
+def test_capped_ranges(d, softcap, q_std):
+    # hidden keys and rows without keys in blocks of small, larger and saturated scores
+    q, k, v, do = _draw(2, 4, 2, 600, d, seed=d + int(softcap), q_std=q_std)
+    check(q, k, v, do, softcap=softcap, key_range=_mixed_ranges(2, 600, d))
+
+
 @pytest.mark.parametrize("d", [64, 256])
 def test_parts_add_up_in_order(d):
     # the same gradient of K and V every time; one key block with all the queries, the rest with few
