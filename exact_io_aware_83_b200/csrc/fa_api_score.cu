@@ -50,8 +50,8 @@ bool score_ready() {
     ok = ok && set_smem(fa::fa_bwd_main_kernel<64, 64, 64, fa::kAttnScoreParts>, fa::BwdLayout<64, 64, 64>::kSmemBytesScore);
     ok = ok && set_smem(fa::fa_bwd_main_kernel<128, 128, 64, fa::kAttnScore>, fa::BwdLayout<128, 128, 64>::kSmemBytesScore);
     ok = ok && set_smem(fa::fa_bwd_main_kernel<128, 128, 64, fa::kAttnScoreParts>, fa::BwdLayout<128, 128, 64>::kSmemBytesScore);
-    ok = ok && set_smem(fa::fa_bwd_main_kernel<256, 128, 32, fa::kAttnScore>, fa::BwdLayout<256, 128, 32>::kSmemBytesScore);
-    ok = ok && set_smem(fa::fa_bwd_main_kernel<256, 128, 32, fa::kAttnScoreParts>, fa::BwdLayout<256, 128, 32>::kSmemBytesScore);
+    ok = ok && set_smem(fa::fa_bwd_main_kernel<256, 128, 64, fa::kAttnScore>, fa::BwdLayout<256, 128, 64>::kSmemBytesScore);
+    ok = ok && set_smem(fa::fa_bwd_main_kernel<256, 128, 64, fa::kAttnScoreParts>, fa::BwdLayout<256, 128, 64>::kSmemBytesScore);
     ok = ok && set_smem(fa::fa_decode_kernel<64, 32, true>, fa::DecodeLayout<64, 32>::kSmemBytes);
     ok = ok && set_smem(fa::fa_decode_kernel<64, 64, true>, fa::DecodeLayout<64, 64>::kSmemBytes);
     ok = ok && set_smem(fa::fa_decode_kernel<64, 128, true>, fa::DecodeLayout<64, 128>::kSmemBytes);
@@ -124,7 +124,7 @@ int check_score_bwd(int B, int N, int d) {
   const long long words = ((N + 127) / 128 + 31) / 32;
   const int cap = d == 64 ? fa::BwdLayout<64, 64, 64>::kScoreBitmapBytes
                   : d == 128 ? fa::BwdLayout<128, 128, 64>::kScoreBitmapBytes
-                             : fa::BwdLayout<256, 128, 32>::kScoreBitmapBytes;
+                             : fa::BwdLayout<256, 128, 64>::kScoreBitmapBytes;
   return words * 4 > cap || B > 65535 ? FA_ERR_UNSUPPORTED : FA_OK;
 }
 
@@ -555,7 +555,7 @@ int fa_bwd_score(const void *q, const void *k, const void *v, const void *o, con
                        make_score(softcap, alibi_slopes, key_range, causal, scale), static_cast<cudaStream_t>(stream)};
   if (d == 64) return launch_bwd_score<64, 64, 64>(a);
   if (d == 128) return launch_bwd_score<128, 128, 64>(a);
-  return launch_bwd_score<256, 128, 32>(a);
+  return launch_bwd_score<256, 128, 64>(a);
 }
 
 int fa_decode_score_num_splits(int B, int Hq, int Hkv, int Nq, int Nk, int d) {

@@ -35,6 +35,10 @@
 // For d = 256 the two K/V accumulators would need all 512 TMEM columns, so two CTAs
 // share each key block, each owning one 128-column half of dK, dV and dQ (both
 // recompute S^T and dP^T over the full d), with 32-row query blocks so the tiles fit.
+// An MMA of 128 keys with 32 query columns takes as long as one with 64 (the A tile's read
+// from shared memory bounds both), so with changed scores the steps have 64 rows, one tile of
+// Q and one of dO: dO_{i+1} is loaded behind dV_i and Q_{i+1} behind dK_i, which exposes the
+// load of Q but halves the MMAs (causal, B = 2, H = 8, N = 4096, cap 50: 1139 -> 821 us).
 #pragma once
 
 #include "fa_common.cuh"
@@ -131,10 +135,13 @@ struct BwdLayout {
   static constexpr int kKTile = kChunks * kKChunk;
   static constexpr int kQChunk = BQ * 128;          // [BQ x 64] bf16 box
   static constexpr int kQTile = kChunks * kQChunk;
-  static constexpr int kQStages = (D == 256) ? 2 : 3;
+  // d = 256 with 64-row steps (changed scores) has room for one Q and one dO tile, with
+  // barriers of their own.
+  static constexpr bool kOneStage = D == 256 && BQ == 64;
+  static constexpr int kQStages = kOneStage ? 1 : (D == 256) ? 2 : 3;
   static constexpr int kDSRowBytes = 128;           // dS^T rows padded to one 128-B swizzle row
   static constexpr int kDSBytes = kKRows * kDSRowBytes;
-  static constexpr int kDQHalves = (BQ * DH * 4 > 32768) ? 2 : 1;  // dQ staging passes
+  static constexpr int kDQHalves = (BQ * DH * 4 > (kOneStage ? 16384 : 32768)) ? 2 : 1;  // dQ staging passes
   static constexpr int kDQCols = DH / kDQHalves;    // d columns staged per pass
   static constexpr int kDQBytes = BQ * kDQCols * 4;
   static constexpr int kOffK = 0;
@@ -159,7 +166,9 @@ struct BwdLayout {
   static constexpr int kBarDQEmpty = kBarDQ + 1;
   static constexpr int kBarFinal = kBarDQEmpty + 1;
   static constexpr int kBarDrain = kBarFinal + 1;
-  static constexpr int kNumBars = kBarDrain + 1;
+  static constexpr int kBarDOFull = kBarDrain + 1;  // kOneStage only
+  static constexpr int kBarDOEmpty = kBarDOFull + 1;
+  static constexpr int kNumBars = kBarDrain + 1 + (kOneStage ? 2 : 0);
   static constexpr int kOffMisc = kOffBar + kNumBars * 8;
   static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
   // Block-sparse variant only: after misc, a 16-byte header (steps counted by each of the
@@ -465,6 +474,61 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
     }
     int issued = 0;
+    if constexpr (L::kOneStage) {
+      // dO_i follows dV_{i-1}, Q_i follows dK_{i-1}; the row values are fetched before that wait.
+      static_assert(SCORE && BQ == 64);
+      int issued_do = 0;
+      for (int i = 0; ok && i < T; ++i) {
+        cur.next();
+        const int h = kvh * g + cur.hh, q0 = cur.q0<BQ>();
+        int c1, c2;
+        q_coords(h, q0, c1, c2);
+        ok = warp_wait_bounded(bar(L::kBarDOEmpty), (i & 1) ^ 1, abort_flag, wait_site(3, L::kBarDOEmpty, i));
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(L::kBarDOFull), L::kQTile);
+#pragma unroll
+          for (int c = 0; c < L::kChunks; ++c)
+            tma_load_3d(sDO + c * L::kQChunk, &tm_do, bar(L::kBarDOFull), c * 64, c1, c2);
+        }
+        ++issued_do;
+        float l[2], dd[2];
+        int lo[2], hi[2];
+        bool whole = true;
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int q = q0 + lane + 32 * x;
+          const bool live = q < sg.Lq;
+          l[x] = live ? p.lse[vec_row(h, q)] * 1.4426950408889634f : INFINITY;
+          dd[x] = live ? p.delta[vec_row(h, q)] : 0.f;
+          if (l[x] == -INFINITY) l[x] = INFINITY;  // a row that sees no key
+          row_range(p.score, b, q, p.N, lo[x], hi[x]);
+          whole = whole && (!live || (lo[x] <= kv0 && hi[x] >= min(kv0 + 128, p.N)));
+        }
+        whole = __all_sync(0xffffffffu, whole);
+        ok = warp_wait_bounded(bar(L::kBarQEmpty), (i & 1) ^ 1, abort_flag, wait_site(3, L::kBarQEmpty, i));
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(bar(L::kBarQFull), L::kQTile);
+#pragma unroll
+          for (int c = 0; c < L::kChunks; ++c)
+            tma_load_3d(sQ + c * L::kQChunk, &tm_q, bar(L::kBarQFull), c * 64, c1, c2);
+          sc_flag[0] = whole;
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int c = lane + 32 * x;
+          vec[c] = l[x];
+          vec[BQ + c] = dd[x];
+          sc_range[c] = lo[x];
+          sc_range[BQ + c] = hi[x];
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::kBarQFull));
+        ++issued;
+      }
+      if (lane == 0 && issued_do > 0) wait_drain(bar(L::kBarDOFull), (issued_do - 1) & 1, 100000000ull);
+    } else {
     for (int i = 0; ok && i < T; ++i) {
       const int st = i % QS, use = i / QS;
       ok = warp_wait_bounded(bar(L::kBarQEmpty + st), (use & 1) ^ 1, abort_flag,
@@ -513,6 +577,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       if (lane == 0) mbar_arrive(bar(L::kBarQFull + st));
       ++issued;
     }
+    }
     if (lane == 0) {
       for (int i = issued > QS ? issued - QS : 0; i < issued; ++i)
         wait_drain(bar(L::kBarQFull + i % QS), (i / QS) & 1, 100000000ull);
@@ -540,8 +605,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         tc_fence_after_sync();
         issue_st(L::kTmS, sK, sQ);
         tc_commit(bar(L::kBarS));
-        issue_st(L::kTmDP, sV, sDO);
-        tc_commit(bar(L::kBarDP));
+        if constexpr (L::kOneStage) {
+          ok = wait_bounded(bar(L::kBarDOFull), 0, abort_flag, wait_site(3, L::kBarDOFull, 0));
+          tc_fence_after_sync();
+        }
+        if (ok) {
+          issue_st(L::kTmDP, sV, sDO);
+          tc_commit(bar(L::kBarDP));
+        }
       }
       for (int i = 0; ok && i < T; ++i) {
         const int st = i % QS;
@@ -554,8 +625,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           mma_ts(tmem + L::kTmDV, tmem + L::kTmS + L::pcol(kk),
                  sdesc_sw128(do_t + (dcol0 / 64) * L::kQChunk + kk * 2048, L::kQChunk, 1024), id_kv,
                  (i > 0 || kk > 0));
+        if constexpr (L::kOneStage) tc_commit(bar(L::kBarDOEmpty));
         // Next step's S^T can start as soon as P^T has been consumed (issue order).
-        if (i + 1 < T) {
+        if (!L::kOneStage && i + 1 < T) {
           const int st1 = (i + 1) % QS;
           if (!(ok = wait_bounded(bar(L::kBarQFull + st1), ((i + 1) / QS) & 1, abort_flag,
                                   wait_site(3, L::kBarQFull + st1, i + 1))))
@@ -572,6 +644,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           mma_ss(tmem + L::kTmDK, sdesc_sw128(sDS + kk * 32, 16, 1024),
                  sdesc_sw128(q_t + (dcol0 / 64) * L::kQChunk + kk * 2048, L::kQChunk, 1024), id_kv,
                  (i > 0 || kk > 0));
+        if constexpr (L::kOneStage) tc_commit(bar(L::kBarQEmpty));
         // dQ_i^T = K^T dS^T : M = 128 d columns, N = BQ, K = 128 keys; both MN-major.
         if (!(ok = wait_bounded(bar(L::kBarDQEmpty), (i & 1) ^ 1, abort_flag,
                                 wait_site(3, L::kBarDQEmpty, i))))
@@ -583,6 +656,19 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                  sdesc_sw128(sDS + kk * 2048, 128 * 128, 1024), id_dq, kk > 0);
         tc_commit(bar(L::kBarDQ));
         tc_commit(bar(L::kBarDSEmpty));
+        if constexpr (L::kOneStage) {
+          if (i + 1 < T) {
+            if (!(ok = wait_bounded(bar(L::kBarQFull), (i + 1) & 1, abort_flag, wait_site(3, L::kBarQFull, i + 1)))) break;
+            tc_fence_after_sync();
+            issue_st(L::kTmS, sK, sQ);
+            tc_commit(bar(L::kBarS));
+            if (!(ok = wait_bounded(bar(L::kBarDOFull), (i + 1) & 1, abort_flag, wait_site(3, L::kBarDOFull, i + 1)))) break;
+            tc_fence_after_sync();
+            issue_st(L::kTmDP, sV, sDO);
+            tc_commit(bar(L::kBarDP));
+          }
+          continue;
+        }
         tc_commit(bar(L::kBarQEmpty + st));
         if (i + 1 < T) {
           issue_st(L::kTmDP, sV, sDO + ((i + 1) % QS) * L::kQTile);
