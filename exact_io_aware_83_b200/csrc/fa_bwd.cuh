@@ -36,9 +36,10 @@
 // share each key block, each owning one 128-column half of dK, dV and dQ (both
 // recompute S^T and dP^T over the full d), with 32-row query blocks so the tiles fit.
 // An MMA of 128 keys with 32 query columns takes as long as one with 64 (the A tile's read
-// from shared memory bounds both), so with changed scores the steps have 64 rows, one tile of
-// Q and one of dO: dO_{i+1} is loaded behind dV_i and Q_{i+1} behind dK_i, which exposes the
-// load of Q but halves the MMAs (causal, B = 2, H = 8, N = 4096, cap 50: 1139 -> 821 us).
+// from shared memory bounds both), so with changed scores the steps have 64 rows.  Two stages
+// of Q and dO fit because V moves to tensor memory, as the A operand of dP^T, and dQ^T shares
+// dP^T's columns.  Causal, B = 2, H = 8, N = 4096, cap 50: 1139 us with 32-row steps, 821 with
+// 64 and one stage of Q and dO, 794 so.
 #pragma once
 
 #include "fa_common.cuh"
@@ -135,18 +136,18 @@ struct BwdLayout {
   static constexpr int kKTile = kChunks * kKChunk;
   static constexpr int kQChunk = BQ * 128;          // [BQ x 64] bf16 box
   static constexpr int kQTile = kChunks * kQChunk;
-  // d = 256 with 64-row steps (changed scores) has room for one Q and one dO tile, with
-  // barriers of their own.
-  static constexpr bool kOneStage = D == 256 && BQ == 64;
-  static constexpr int kQStages = kOneStage ? 1 : (D == 256) ? 2 : 3;
+  // d = 256 with 64-row steps (changed scores): V moves to tensor memory before the first
+  // step, and its shared memory is the second stage of Q and of dO; dQ^T takes dP^T's columns.
+  static constexpr bool kVInTmem = D == 256 && BQ == 64;
+  static constexpr int kQStages = (D == 256) ? 2 : 3;
   static constexpr int kDSRowBytes = 128;           // dS^T rows padded to one 128-B swizzle row
   static constexpr int kDSBytes = kKRows * kDSRowBytes;
-  static constexpr int kDQHalves = (BQ * DH * 4 > (kOneStage ? 16384 : 32768)) ? 2 : 1;  // dQ staging passes
+  static constexpr int kDQHalves = (BQ * DH * 4 > (kVInTmem ? 16384 : 32768)) ? 2 : 1;  // dQ staging passes
   static constexpr int kDQCols = DH / kDQHalves;    // d columns staged per pass
   static constexpr int kDQBytes = BQ * kDQCols * 4;
   static constexpr int kOffK = 0;
-  static constexpr int kOffV = kOffK + kKTile;
-  static constexpr int kOffQ = kOffV + kKTile;                // Q ring
+  static constexpr int kOffV = kOffK + kKTile + (kVInTmem ? kQTile : 0);
+  static constexpr int kOffQ = kVInTmem ? kOffK + kKTile : kOffV + kKTile;  // Q ring
   static constexpr int kOffDO = kOffQ + kQStages * kQTile;    // dO ring
   static constexpr int kOffDS = kOffDO + kQStages * kQTile;
   static constexpr int kOffDQ = kOffDS + kDSBytes;
@@ -166,10 +167,9 @@ struct BwdLayout {
   static constexpr int kBarDQEmpty = kBarDQ + 1;
   static constexpr int kBarFinal = kBarDQEmpty + 1;
   static constexpr int kBarDrain = kBarFinal + 1;
-  static constexpr int kBarDOFull = kBarDrain + 1;  // kOneStage only
-  static constexpr int kBarDOEmpty = kBarDOFull + 1;
-  static constexpr int kNumBars = kBarDrain + 1 + (kOneStage ? 2 : 0);
-  static constexpr int kOffMisc = kOffBar + kNumBars * 8;
+  static constexpr int kBarV = kBarDrain + 1;  // kVInTmem only: V is in tensor memory
+  static constexpr int kNumBars = kBarDrain + 1 + (kVInTmem ? 1 : 0);
+  static constexpr int kOffMisc = kOffBar + (kNumBars * 8 + 15) / 16 * 16;
   static constexpr int kSmemBytes = kOffMisc + 16 + 1024;
   // Block-sparse variant only: after misc, a 16-byte header (steps counted by each of the
   // four warps that build it) and a bitmap per query head of the group: bit qb of head hh
@@ -181,8 +181,9 @@ struct BwdLayout {
   // Changed scores only: after the header, per stage the first visible key and the end of the
   // visible keys of each query row, and a flag (every row sees the whole key block); then
   // one bitmap of query blocks, the same for every head of the group.
+  // (kVInTmem: [stage][BQ] words of both bounds, counted from the key block's first key)
   static constexpr int kOffRange = kOffList + 16;                  // [stage][lo | hi][BQ] int
-  static constexpr int kOffScoreFlag = kOffRange + kQStages * 2 * BQ * 4;  // [stage], padded to 16 bytes
+  static constexpr int kOffScoreFlag = kOffRange + kQStages * (kVInTmem ? 1 : 2) * BQ * 4;  // [stage], padded to 16 bytes
   static constexpr int kOffScoreBits = kOffScoreFlag + 16;
   static constexpr int kScoreBitmapBytes =
       (232448 - (kOffScoreBits + 1024)) / 4 * 4 < 8192 ? (232448 - (kOffScoreBits + 1024)) / 4 * 4 : 8192;
@@ -192,7 +193,8 @@ struct BwdLayout {
   static constexpr uint32_t kTmDK = DH;
   static constexpr uint32_t kTmS = 2 * DH;
   static constexpr uint32_t kTmDP = 2 * DH + BQ;
-  static constexpr uint32_t kTmDQ = 2 * DH + 2 * BQ;
+  static constexpr uint32_t kTmDQ = kVInTmem ? kTmDP : 2 * DH + 2 * BQ;
+  static constexpr uint32_t kTmV = 2 * DH + 2 * BQ;  // kVInTmem only: bf16 pairs, D / 2 columns
   static constexpr uint32_t kTmemCols = 512;
   // Elementwise work is split between two warpgroups by query column: each owns HC of
   // the BQ columns of every key row.  Its bf16 P^T half is packed into the first HC/2
@@ -203,7 +205,7 @@ struct BwdLayout {
   __host__ __device__ static constexpr uint32_t pcol(int kk) {
     return static_cast<uint32_t>((kk / kKStepsPerHalf) * kHC + (kk % kKStepsPerHalf) * 8);
   }
-  static_assert(kTmDQ + BQ <= 512, "tensor-memory budget");
+  static_assert(kTmDQ + BQ <= 512 && (!kVInTmem || kTmV + D / 2 <= 512), "tensor-memory budget");
   static_assert(kSmemBytesSparse <= 232448 && kSparseBitmapBytes >= 256, "shared-memory budget");
   static_assert(kSmemBytesScore <= 232448 && kScoreBitmapBytes >= 256 && kOffRange % 16 == 0, "shared-memory budget");
   static_assert(BQ == 32 || BQ == 64, "query block");
@@ -300,6 +302,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   const uint32_t sK = base + L::kOffK, sV = base + L::kOffV;
   const uint32_t sQ = base + L::kOffQ, sDO = base + L::kOffDO;
   const uint32_t sDS = base + L::kOffDS, sDQ = base + L::kOffDQ;
+  // dO stage st (kVInTmem: in reverse, so that stage 1 lies next to that of Q, where V was)
+  auto do_tile = [&](int st) { return sDO + (L::kVInTmem ? 1 - st : st) * L::kQTile; };
 
   const int warp = threadIdx.x / 32;
   const int lane = threadIdx.x % 32;
@@ -370,6 +374,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       uint32_t cnt = 1;
       if (i == L::kBarP || i == L::kBarDS) cnt = 8;   // one arrival per elementwise warp
       if (i == L::kBarDQEmpty) cnt = 4;               // one per dQ-drain warp
+      if (L::kVInTmem && i == L::kBarV) cnt = 8;
       // Q/dO stages: the TMA expect-tx arrival plus the arrival after the LSE / Delta stores.
       if (i >= L::kBarQFull && i < L::kBarQFull + QS) cnt = 2;
       mbar_init(bar(i), cnt);
@@ -474,66 +479,14 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
     }
     int issued = 0;
-    if constexpr (L::kOneStage) {
-      // dO_i follows dV_{i-1}, Q_i follows dK_{i-1}; the row values are fetched before that wait.
-      static_assert(SCORE && BQ == 64);
-      int issued_do = 0;
-      for (int i = 0; ok && i < T; ++i) {
-        cur.next();
-        const int h = kvh * g + cur.hh, q0 = cur.q0<BQ>();
-        int c1, c2;
-        q_coords(h, q0, c1, c2);
-        ok = warp_wait_bounded(bar(L::kBarDOEmpty), (i & 1) ^ 1, abort_flag, wait_site(3, L::kBarDOEmpty, i));
-        if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(bar(L::kBarDOFull), L::kQTile);
-#pragma unroll
-          for (int c = 0; c < L::kChunks; ++c)
-            tma_load_3d(sDO + c * L::kQChunk, &tm_do, bar(L::kBarDOFull), c * 64, c1, c2);
-        }
-        ++issued_do;
-        float l[2], dd[2];
-        int lo[2], hi[2];
-        bool whole = true;
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int q = q0 + lane + 32 * x;
-          const bool live = q < sg.Lq;
-          l[x] = live ? p.lse[vec_row(h, q)] * 1.4426950408889634f : INFINITY;
-          dd[x] = live ? p.delta[vec_row(h, q)] : 0.f;
-          if (l[x] == -INFINITY) l[x] = INFINITY;  // a row that sees no key
-          row_range(p.score, b, q, p.N, lo[x], hi[x]);
-          whole = whole && (!live || (lo[x] <= kv0 && hi[x] >= min(kv0 + 128, p.N)));
-        }
-        whole = __all_sync(0xffffffffu, whole);
-        ok = warp_wait_bounded(bar(L::kBarQEmpty), (i & 1) ^ 1, abort_flag, wait_site(3, L::kBarQEmpty, i));
-        if (!ok) break;
-        if (lane == 0) {
-          mbar_arrive_expect_tx(bar(L::kBarQFull), L::kQTile);
-#pragma unroll
-          for (int c = 0; c < L::kChunks; ++c)
-            tma_load_3d(sQ + c * L::kQChunk, &tm_q, bar(L::kBarQFull), c * 64, c1, c2);
-          sc_flag[0] = whole;
-        }
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int c = lane + 32 * x;
-          vec[c] = l[x];
-          vec[BQ + c] = dd[x];
-          sc_range[c] = lo[x];
-          sc_range[BQ + c] = hi[x];
-        }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(bar(L::kBarQFull));
-        ++issued;
-      }
-      if (lane == 0 && issued_do > 0) wait_drain(bar(L::kBarDOFull), (issued_do - 1) & 1, 100000000ull);
-    } else {
     for (int i = 0; ok && i < T; ++i) {
       const int st = i % QS, use = i / QS;
       ok = warp_wait_bounded(bar(L::kBarQEmpty + st), (use & 1) ^ 1, abort_flag,
                              wait_site(3, L::kBarQEmpty + st, i));
       if (!ok) break;
+      if constexpr (L::kVInTmem) {
+        if (i == 1 && !(ok = warp_wait_bounded(bar(L::kBarV), 0, abort_flag, wait_site(3, L::kBarV, i)))) break;
+      }
       if constexpr (LISTED) cur.next();
       const int h = LISTED ? kvh * g + cur.hh : step_head(i), q0 = LISTED ? cur.q0<BQ>() : step_q0(i);
       if (lane == 0) {
@@ -543,7 +496,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
         for (int c = 0; c < L::kChunks; ++c) {
           tma_load_3d(sQ + st * L::kQTile + c * L::kQChunk, &tm_q, bar(L::kBarQFull + st), c * 64, c1, c2);
-          tma_load_3d(sDO + st * L::kQTile + c * L::kQChunk, &tm_do, bar(L::kBarQFull + st), c * 64, c1, c2);
+          tma_load_3d(do_tile(st) + c * L::kQChunk, &tm_do, bar(L::kBarQFull + st), c * 64, c1, c2);
         }
       }
       float *lse2 = vec + (st * 2) * BQ;
@@ -562,8 +515,12 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           if (lse2[c] == -INFINITY) lse2[c] = INFINITY;
           int lo, hi;
           row_range(p.score, b, q, p.N, lo, hi);
-          sc_range[(st * 2) * BQ + c] = lo;
-          sc_range[(st * 2 + 1) * BQ + c] = hi;
+          if constexpr (L::kVInTmem) {
+            sc_range[st * BQ + c] = min(max(lo - kv0, 0), 128) | min(max(hi - kv0, 0), 128) << 16;
+          } else {
+            sc_range[(st * 2) * BQ + c] = lo;
+            sc_range[(st * 2 + 1) * BQ + c] = hi;
+          }
           whole = whole && (!live || (lo <= kv0 && hi >= min(kv0 + 128, p.N)));
         }
       }
@@ -576,7 +533,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::kBarQFull + st));
       ++issued;
-    }
     }
     if (lane == 0) {
       for (int i = issued > QS ? issued - QS : 0; i < issued; ++i)
@@ -599,24 +555,35 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           mma_ss(tmem + dst, sdesc_sw128(a0 + oa, 16, 1024), sdesc_sw128(b0 + ob, 16, 1024), id_st, kk > 0);
         }
       };
+      // dP^T of the dO tile in stage st: A = V from shared or from tensor memory.
+      auto issue_dp = [&](int st) {
+        if constexpr (L::kVInTmem) {
+#pragma unroll
+          for (int kk = 0; kk < D / 16; ++kk)
+            mma_ts(tmem + L::kTmDP, tmem + L::kTmV + kk * 8,
+                   sdesc_sw128(do_tile(st) + (kk / 4) * L::kQChunk + (kk % 4) * 32, 16, 1024), id_st, kk > 0);
+        } else {
+          issue_st(L::kTmDP, sV, do_tile(st));
+        }
+      };
       bool ok = wait_bounded(bar(L::kBarKV), 0, abort_flag, wait_site(3, L::kBarKV, 0));
       if (ok && (!GENLIKE || T > 0)) ok = wait_bounded(bar(L::kBarQFull), 0, abort_flag, wait_site(3, L::kBarQFull, 0));
       if (ok && (!GENLIKE || T > 0)) {
         tc_fence_after_sync();
         issue_st(L::kTmS, sK, sQ);
         tc_commit(bar(L::kBarS));
-        if constexpr (L::kOneStage) {
-          ok = wait_bounded(bar(L::kBarDOFull), 0, abort_flag, wait_site(3, L::kBarDOFull, 0));
+        if constexpr (L::kVInTmem) {
+          ok = wait_bounded(bar(L::kBarV), 0, abort_flag, wait_site(3, L::kBarV, 0));
           tc_fence_after_sync();
         }
         if (ok) {
-          issue_st(L::kTmDP, sV, sDO);
+          issue_dp(0);
           tc_commit(bar(L::kBarDP));
         }
       }
       for (int i = 0; ok && i < T; ++i) {
         const int st = i % QS;
-        const uint32_t q_t = sQ + st * L::kQTile, do_t = sDO + st * L::kQTile;
+        const uint32_t q_t = sQ + st * L::kQTile, do_t = do_tile(st);
         // dV += P^T dO_i : M = 128 keys, N = DH, K = BQ queries; P^T (bf16) in TMEM.
         if (!(ok = wait_bounded(bar(L::kBarP), i & 1, abort_flag, wait_site(3, L::kBarP, i)))) break;
         tc_fence_after_sync();
@@ -625,9 +592,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           mma_ts(tmem + L::kTmDV, tmem + L::kTmS + L::pcol(kk),
                  sdesc_sw128(do_t + (dcol0 / 64) * L::kQChunk + kk * 2048, L::kQChunk, 1024), id_kv,
                  (i > 0 || kk > 0));
-        if constexpr (L::kOneStage) tc_commit(bar(L::kBarDOEmpty));
         // Next step's S^T can start as soon as P^T has been consumed (issue order).
-        if (!L::kOneStage && i + 1 < T) {
+        if (i + 1 < T) {
           const int st1 = (i + 1) % QS;
           if (!(ok = wait_bounded(bar(L::kBarQFull + st1), ((i + 1) / QS) & 1, abort_flag,
                                   wait_site(3, L::kBarQFull + st1, i + 1))))
@@ -644,7 +610,6 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           mma_ss(tmem + L::kTmDK, sdesc_sw128(sDS + kk * 32, 16, 1024),
                  sdesc_sw128(q_t + (dcol0 / 64) * L::kQChunk + kk * 2048, L::kQChunk, 1024), id_kv,
                  (i > 0 || kk > 0));
-        if constexpr (L::kOneStage) tc_commit(bar(L::kBarQEmpty));
         // dQ_i^T = K^T dS^T : M = 128 d columns, N = BQ, K = 128 keys; both MN-major.
         if (!(ok = wait_bounded(bar(L::kBarDQEmpty), (i & 1) ^ 1, abort_flag,
                                 wait_site(3, L::kBarDQEmpty, i))))
@@ -656,22 +621,13 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                  sdesc_sw128(sDS + kk * 2048, 128 * 128, 1024), id_dq, kk > 0);
         tc_commit(bar(L::kBarDQ));
         tc_commit(bar(L::kBarDSEmpty));
-        if constexpr (L::kOneStage) {
-          if (i + 1 < T) {
-            if (!(ok = wait_bounded(bar(L::kBarQFull), (i + 1) & 1, abort_flag, wait_site(3, L::kBarQFull, i + 1)))) break;
-            tc_fence_after_sync();
-            issue_st(L::kTmS, sK, sQ);
-            tc_commit(bar(L::kBarS));
-            if (!(ok = wait_bounded(bar(L::kBarDOFull), (i + 1) & 1, abort_flag, wait_site(3, L::kBarDOFull, i + 1)))) break;
-            tc_fence_after_sync();
-            issue_st(L::kTmDP, sV, sDO);
-            tc_commit(bar(L::kBarDP));
-          }
-          continue;
-        }
         tc_commit(bar(L::kBarQEmpty + st));
         if (i + 1 < T) {
-          issue_st(L::kTmDP, sV, sDO + ((i + 1) % QS) * L::kQTile);
+          if constexpr (L::kVInTmem) {  // dQ_i has left its columns
+            if (!(ok = wait_bounded(bar(L::kBarDQEmpty), i & 1, abort_flag, wait_site(3, L::kBarDQEmpty, i)))) break;
+            tc_fence_after_sync();
+          }
+          issue_dp((i + 1) % QS);
           tc_commit(bar(L::kBarDP));
         }
       }
@@ -694,6 +650,24 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     const bool row_live = kv < sg.Lk;
     const float sl2 = p.sl2;
     bool ok = true;
+    if constexpr (L::kVInTmem) {  // V, row r: chunk (64 columns) 2 wg and 2 wg + 1
+      ok = warp_wait_bounded(bar(L::kBarKV), 0, abort_flag, wait_site(3, L::kBarKV, 0));
+      if (ok) {
+#pragma unroll
+        for (int c = 2 * wg; c < 2 * wg + 2; ++c) {
+          uint32_t w[32];
+#pragma unroll
+          for (int u = 0; u < 8; ++u)
+            ld_shared_v4(sV + c * L::kKChunk + r * 128 + ((u ^ (r & 7)) * 16), w[4 * u], w[4 * u + 1], w[4 * u + 2],
+                         w[4 * u + 3]);
+          tmem_st_x32(tmem + L::kTmV + lane_off + c * 32, w);
+        }
+        tmem_wait_st();
+        tc_fence_before_sync();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(L::kBarV));
+      }
+    }
     for (int i = 0; ok && i < T; ++i) {
       const int st = i % QS;
       if constexpr (LISTED) cur.next();
@@ -726,7 +700,15 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           if (part || !row_live) {
 #pragma unroll
             for (int c = 0; c < HC; c += 4) {
-              const int4 lo = lo4[c / 4], hi = hi4[c / 4];
+              int4 lo, hi;
+              if constexpr (L::kVInTmem) {
+                const int4 w = reinterpret_cast<const int4 *>(sc_range + st * BQ + c0)[c / 4];
+                lo = make_int4(kv0 + (w.x & 0xFFFF), kv0 + (w.y & 0xFFFF), kv0 + (w.z & 0xFFFF), kv0 + (w.w & 0xFFFF));
+                hi = make_int4(kv0 + (w.x >> 16), kv0 + (w.y >> 16), kv0 + (w.z >> 16), kv0 + (w.w >> 16));
+              } else {
+                lo = lo4[c / 4];
+                hi = hi4[c / 4];
+              }
               const bool see[4] = {row_live && kv >= lo.x && kv < hi.x, row_live && kv >= lo.y && kv < hi.y,
                                    row_live && kv >= lo.z && kv < hi.z, row_live && kv >= lo.w && kv < hi.w};
 #pragma unroll

@@ -271,7 +271,7 @@ size_t fa_bwd_score_workspace_bytes(int B, int Hq, int Hkv, int N, int d);
  * it): arguments as fa_bwd otherwise.  dS = P (dP - Delta) (1 - tanh^2(x / softcap)).  The
  * slopes and ranges are constants: they get no gradient.  Keys that no query sees get
  * dK = dV = 0, rows without keys dQ = 0.  Limits: B <= 65535; N below about 8 million
- * (d = 64, 128) or 880 thousand (d = 256) rows, by the bitmap of query blocks in shared memory
+ * (d = 64, 128) or 344 thousand (d = 256) rows, by the bitmap of query blocks in shared memory
  * (FA_ERR_UNSUPPORTED beyond).
  */
 int fa_bwd_score(const void *q, const void *k, const void *v, const void *o, const float *lse,
