@@ -445,7 +445,7 @@ int fa_merge(const float *o_parts, const float *lse_parts, void *o, float *lse, 
              int rows, int d, void *stream);
 
 /*
- * Synchronises `stream`, returns the device status word of the current device
+ * Synchronises `stream`, returns the device status of the current device
  * (FA_OK, FA_ERR_DEVICE_TIMEOUT or FA_ERR_SEQLENS) and clears it.  Returns FA_ERR_CUDA if the
  * synchronisation itself fails.
  */
@@ -453,8 +453,8 @@ int fa_device_status(void *stream);
 
 /*
  * Kernel timing for benchmarks.  fa_kernel_timing(1) resets the counters and makes every
- * later fa_fwd / fa_bwd / fa_decode call (and their window, varlen, dropout and
- * block-sparse forms, and fa_bwd_noalloc) in this process record
+ * later fa_fwd / fa_bwd / fa_decode call (and their window, varlen, dropout, block-sparse
+ * and changed-score forms, fa_bwd_noalloc and fa_decode_kv4) in this process record
  * a pair of CUDA events (created by the
  * library, no device memory) around its main attention kernel, on the call's stream;
  * fa_kernel_timing(0) stops recording.  fa_kernel_time_ms(which, &ms, &launches)
