@@ -39,7 +39,7 @@
 // from shared memory bounds both), so with changed scores the steps have 64 rows.  Two stages
 // of Q and dO fit because V moves to tensor memory, as the A operand of dP^T, and dQ^T shares
 // dP^T's columns.  Causal, B = 2, H = 8, N = 4096, cap 50: 1139 us with 32-row steps, 821 with
-// 64 and one stage of Q and dO, 794 so.
+// 64 and one stage of Q and dO, 794-814 so (documents of 300 rows: 165, 138 and 123).
 #pragma once
 
 #include "fa_common.cuh"
@@ -479,14 +479,71 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       }
     }
     int issued = 0;
+    if constexpr (L::kVInTmem) {
+      // The row values of a step are fetched before the wait for its stage: with two stages
+      // they were on its path (causal documents, B = 2, Hq = 8, Hkv = 4, N = 2048: 204 -> 188 us;
+      // prefixes, B = 2, H = 8, N = 4096: 947 -> 835; no ranges +-2%).  With three stages they
+      // are not, and the values held cost registers (d = 128, cap 50: 556 -> 592).
+      static_assert(SCORE);
+      constexpr int kPer = BQ / 32;
+      float lse_r[kPer], dl_r[kPer];
+      int lo[kPer], hi[kPer], h = 0, q0 = 0;
+      auto fetch = [&]() {
+        cur.next();
+        h = kvh * g + cur.hh;
+        q0 = cur.q0<BQ>();
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) {
+          const int q = q0 + lane + 32 * x;
+          const bool live = q < sg.Lq;
+          lse_r[x] = live ? p.lse[vec_row(h, q)] : INFINITY;
+          dl_r[x] = live ? p.delta[vec_row(h, q)] : 0.f;
+          row_range(p.score, b, q, p.N, lo[x], hi[x]);
+        }
+      };
+      if (T > 0) fetch();
+      for (int i = 0; ok && i < T; ++i) {
+        const int st = i % QS, use = i / QS;
+        ok = warp_wait_bounded(bar(L::kBarQEmpty + st), (use & 1) ^ 1, abort_flag,
+                               wait_site(3, L::kBarQEmpty + st, i));
+        if (!ok) break;
+        if (i == 1 && !(ok = warp_wait_bounded(bar(L::kBarV), 0, abort_flag, wait_site(3, L::kBarV, i)))) break;
+        if (lane == 0) {
+          int c1, c2;
+          q_coords(h, q0, c1, c2);
+          mbar_arrive_expect_tx(bar(L::kBarQFull + st), 2 * L::kQTile);
+#pragma unroll
+          for (int c = 0; c < L::kChunks; ++c) {
+            tma_load_3d(sQ + st * L::kQTile + c * L::kQChunk, &tm_q, bar(L::kBarQFull + st), c * 64, c1, c2);
+            tma_load_3d(do_tile(st) + c * L::kQChunk, &tm_do, bar(L::kBarQFull + st), c * 64, c1, c2);
+          }
+        }
+        float *lse2 = vec + (st * 2) * BQ;
+        float *dl = vec + (st * 2 + 1) * BQ;
+        bool whole = true;  // every row of the step sees the whole key block
+#pragma unroll
+        for (int x = 0; x < kPer; ++x) {
+          const int c = lane + 32 * x;
+          // Rows past the sequence get LSE = +inf, so their probabilities are exactly 0; so does
+          // a row that sees no key (LSE = -inf), which may share a block with rows that do.
+          lse2[c] = lse_r[x] == -INFINITY ? INFINITY : lse_r[x] * 1.4426950408889634f;
+          dl[c] = dl_r[x];
+          sc_range[st * BQ + c] = min(max(lo[x] - kv0, 0), 128) | min(max(hi[x] - kv0, 0), 128) << 16;
+          whole = whole && (q0 + c >= sg.Lq || (lo[x] <= kv0 && hi[x] >= min(kv0 + 128, p.N)));
+        }
+        whole = __all_sync(0xffffffffu, whole);
+        if (lane == 0) sc_flag[st] = whole;
+        __syncwarp();  // orders the stores before the arrival
+        if (lane == 0) mbar_arrive(bar(L::kBarQFull + st));
+        ++issued;
+        if (i + 1 < T) fetch();
+      }
+    } else {
     for (int i = 0; ok && i < T; ++i) {
       const int st = i % QS, use = i / QS;
       ok = warp_wait_bounded(bar(L::kBarQEmpty + st), (use & 1) ^ 1, abort_flag,
                              wait_site(3, L::kBarQEmpty + st, i));
       if (!ok) break;
-      if constexpr (L::kVInTmem) {
-        if (i == 1 && !(ok = warp_wait_bounded(bar(L::kBarV), 0, abort_flag, wait_site(3, L::kBarV, i)))) break;
-      }
       if constexpr (LISTED) cur.next();
       const int h = LISTED ? kvh * g + cur.hh : step_head(i), q0 = LISTED ? cur.q0<BQ>() : step_q0(i);
       if (lane == 0) {
@@ -496,7 +553,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
         for (int c = 0; c < L::kChunks; ++c) {
           tma_load_3d(sQ + st * L::kQTile + c * L::kQChunk, &tm_q, bar(L::kBarQFull + st), c * 64, c1, c2);
-          tma_load_3d(do_tile(st) + c * L::kQChunk, &tm_do, bar(L::kBarQFull + st), c * 64, c1, c2);
+          tma_load_3d(sDO + st * L::kQTile + c * L::kQChunk, &tm_do, bar(L::kBarQFull + st), c * 64, c1, c2);
         }
       }
       float *lse2 = vec + (st * 2) * BQ;
@@ -515,12 +572,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           if (lse2[c] == -INFINITY) lse2[c] = INFINITY;
           int lo, hi;
           row_range(p.score, b, q, p.N, lo, hi);
-          if constexpr (L::kVInTmem) {
-            sc_range[st * BQ + c] = min(max(lo - kv0, 0), 128) | min(max(hi - kv0, 0), 128) << 16;
-          } else {
-            sc_range[(st * 2) * BQ + c] = lo;
-            sc_range[(st * 2 + 1) * BQ + c] = hi;
-          }
+          sc_range[(st * 2) * BQ + c] = lo;
+          sc_range[(st * 2 + 1) * BQ + c] = hi;
           whole = whole && (!live || (lo <= kv0 && hi >= min(kv0 + 128, p.N)));
         }
       }
@@ -533,6 +586,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(L::kBarQFull + st));
       ++issued;
+    }
     }
     if (lane == 0) {
       for (int i = issued > QS ? issued - QS : 0; i < issued; ++i)
