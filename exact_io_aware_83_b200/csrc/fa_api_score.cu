@@ -163,9 +163,6 @@ int launch_bwd_score(const BwdScoreArgs &a) {
   float *dqacc = reinterpret_cast<float *>(static_cast<char *>(a.workspace) + fa::pad256(static_cast<size_t>(rows) * 4));
   const long long hq = static_cast<long long>(a.B) * a.Hq, hkv = static_cast<long long>(a.B) * a.Hkv;
 
-  fa::fa_bwd_pre_kernel<D><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, a.s>>>(
-      static_cast<const __nv_bfloat16 *>(a.o), static_cast<const __nv_bfloat16 *>(a.dout), delta, dqacc, rows);
-
   fa::BwdParams p{};
   p.lse = a.lse;
   p.delta = delta;
@@ -186,16 +183,20 @@ int launch_bwd_score(const BwdScoreArgs &a) {
   const fa::PlanLayout plan = fa::plan_layout(a.B, a.Hkv, a.N, D, max_parts);
   behind += fa::pad256(static_cast<size_t>(a.B) * p.nkb * 8);
   int *parts = reinterpret_cast<int *>(behind + plan.parts);
+  const auto *ob = static_cast<const __nv_bfloat16 *>(a.o), *dob = static_cast<const __nv_bfloat16 *>(a.dout);
   if (max_parts > 0) {
     int4 *items = reinterpret_cast<int4 *>(behind + plan.items);
-    fa::fa_bwd_plan_kernel<<<1, fa::kPlanThreads, 0, a.s>>>(a.score, a.B, a.N, p.nkb, a.Hq / a.Hkv, 128 / BQ,
-                                                          (a.N - (p.nkb - 1) * 128 + BQ - 1) / BQ, a.Hkv * (D / DH),
-                                                          max_parts, D == 256 ? 6 : 12, blocks, parts, items);
+    const fa::PlanParams pp{a.score, a.B, a.N, p.nkb, a.Hq / a.Hkv, 128 / BQ, (a.N - (p.nkb - 1) * 128 + BQ - 1) / BQ,
+                            a.Hkv * (D / DH), max_parts, D == 256 ? 6 : 12, blocks, parts, items};
+    const long long ctas = 1 + (rows + fa::kPlanThreads / 32 - 1) / (fa::kPlanThreads / 32);
+    fa::fa_bwd_plan_kernel<D><<<static_cast<unsigned>(ctas), fa::kPlanThreads, 0, a.s>>>(pp, ob, dob, delta, dqacc, rows);
     p.items = items;
     p.parts = reinterpret_cast<float *>(behind + plan.sums);
-  } else if (a.score.range) {
-    fa::fa_score_blocks_kernel<<<dim3(static_cast<unsigned>(p.nkb), static_cast<unsigned>(a.B)), 128, 0, a.s>>>(
-        a.score, a.N, blocks);
+  } else {
+    fa::fa_bwd_pre_kernel<D><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, a.s>>>(ob, dob, delta, dqacc, rows);
+    if (a.score.range)
+      fa::fa_score_blocks_kernel<<<dim3(static_cast<unsigned>(p.nkb), static_cast<unsigned>(a.B)), 128, 0, a.s>>>(
+          a.score, a.N, blocks);
   }
   if (a.score.range) p.blocks = blocks;
   const fa::BwdOrder order = bwd_order(a.B, a.Hkv, a.N, a.score.range ? a.N : -1, a.right);

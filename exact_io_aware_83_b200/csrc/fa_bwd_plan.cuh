@@ -14,13 +14,13 @@
 //          (K, V, the pipeline's start, the epilogue, the sums), the parts share the SMs evenly,
 //          and the last one runs on for half a part; or the longest part alone when all fit at once;
 //   order  the parts by length, longest first.
-// Whole calls, us, without and with it: B = 2, Hq = 6, Hkv = 2, N = 1000, d = 64, prefixes and
-// slopes 94 and
-// 34; B = 1, Hq = 8, Hkv = 1, N = 4096, d = 128, causal, cap 50 991 and 173; B = 1, H = 4,
-// N = 4096, d = 128, prefixes 135 and 102.  With more units it is left out: cutting cost more than it
-// levelled (B = 2, H = 4, N = 4096, d = 128, documents of 400 rows: 70 us whole, 91 in halves),
-// and the order alone gave up the locality of a head's key blocks (B = 4, Hq = 32, Hkv = 8,
-// N = 4096, documents of 500 rows: 697 us in unit_order's order, 781 longest first).
+// Calls in a graph, us, without and with it: B = 2, Hq = 6, Hkv = 2, N = 1000, d = 64, prefixes
+// and slopes 94 and 32; B = 1, Hq = 8, Hkv = 1, N = 4096, d = 128, causal, cap 50, 991 and 160;
+// B = 1, H = 4, N = 4096, d = 128, prefixes and slopes, 135 and 99.  With more units it is left
+// out: cutting cost more than it levelled (B = 2, H = 4, N = 4096, d = 128, documents of 400
+// rows: 70 us whole, 91 in halves), and the order alone gave up the locality of a head's key
+// blocks (B = 4, Hq = 32, Hkv = 8, N = 4096, documents of 500 rows: 697 us in unit_order's order,
+// 781 longest first).
 #pragma once
 
 #include "fa_bwd.cuh"
@@ -53,13 +53,26 @@ inline PlanLayout plan_layout(int B, int Hkv, int N, int d, int max_parts) {
   return l;
 }
 
-// One CTA; B nkb < kPlanSMs.  heads: CTAs per part (K/V heads, times the halves of d = 256);
-// nsub, nsub_last: steps per 128-row query block and in the last one; g: query heads per K/V
-// head.  Writes the spans of the query blocks, the parts of each key block and max_parts B nkb
-// items, those behind the last part with no parts.
-static __global__ void __launch_bounds__(kPlanThreads)
-    fa_bwd_plan_kernel(const ScoreCfg cfg, int B, int N, int nkb, int g, int nsub, int nsub_last, int heads,
-                       int max_parts, int part_steps, int2 *blocks, int *parts, int4 *items) {
+struct PlanParams {
+  ScoreCfg cfg;
+  int B, N, nkb, g;     // g: query heads per K/V head
+  int nsub, nsub_last;  // steps per 128-row query block and in the last one
+  int heads;            // CTAs per part: K/V heads, times the halves of d = 256
+  int max_parts, part_steps;
+  int2 *blocks;
+  int *parts;
+  int4 *items;
+};
+
+// The plan, by one CTA; B nkb < kPlanSMs.  Writes the spans of the query blocks, the parts of each
+// key block and max_parts B nkb items, those behind the last part with no parts.
+__device__ __forceinline__ void bwd_plan(const PlanParams &p) {
+  const ScoreCfg &cfg = p.cfg;
+  const int B = p.B, N = p.N, nkb = p.nkb, g = p.g, nsub = p.nsub, nsub_last = p.nsub_last, heads = p.heads;
+  const int max_parts = p.max_parts, part_steps = p.part_steps;
+  int2 *blocks = p.blocks;
+  int *parts = p.parts;
+  int4 *items = p.items;
   __shared__ int2 span[kPlanSMs];
   __shared__ int steps[kPlanSMs];
   __shared__ float cost[kPlanMaxParts];
@@ -129,6 +142,36 @@ static __global__ void __launch_bounds__(kPlanThreads)
     if (e == 0)
       for (int i = all + lane; i < entries * max_parts; i += 32) items[i] = make_int4(0, 0, 0, 0);
   }
+}
+
+// The first kernel of a backward with a plan: block 0 makes the plan, the others do what
+// fa_bwd_pre_kernel does (Delta_i = <dO_i, O_i>, a zeroed dQ accumulator), a warp per row.  (One
+// after the other they took 4 and 8 us and a launch more.)
+template <int D>
+static __global__ void __launch_bounds__(kPlanThreads, 2)
+    fa_bwd_plan_kernel(const PlanParams plan, const __nv_bfloat16 *__restrict__ o, const __nv_bfloat16 *__restrict__ dout,
+                       float *__restrict__ delta, float *__restrict__ dqacc, long long rows) {
+  if (blockIdx.x == 0) {
+    bwd_plan(plan);
+    return;
+  }
+  constexpr int kPairs = D / 64;  // bf16 pairs per lane
+  const int lane = threadIdx.x % 32;
+  const long long row = static_cast<long long>(blockIdx.x - 1) * (kPlanThreads / 32) + threadIdx.x / 32;
+  if (row >= rows) return;
+  const __nv_bfloat162 *orow = reinterpret_cast<const __nv_bfloat162 *>(o + row * D) + lane * kPairs;
+  const __nv_bfloat162 *drow = reinterpret_cast<const __nv_bfloat162 *>(dout + row * D) + lane * kPairs;
+  float acc = 0.f;
+#pragma unroll
+  for (int e = 0; e < kPairs; ++e) {
+    const float2 a = __bfloat1622float2(orow[e]), c = __bfloat1622float2(drow[e]);
+    acc += a.x * c.x + a.y * c.y;
+  }
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, off);
+  if (lane == 0) delta[row] = acc;
+#pragma unroll
+  for (int c = lane * 4; c < D; c += 128) *reinterpret_cast<float4 *>(dqacc + row * D + c) = make_float4(0.f, 0.f, 0.f, 0.f);
 }
 
 // dQ = bf16(scale dQacc), and dV = bf16(sum of the parts), dK = bf16(scale sum of the parts) for
