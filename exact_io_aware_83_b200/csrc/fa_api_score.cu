@@ -118,14 +118,13 @@ fa::ScoreCfg make_score(float softcap, const float *slopes, const int *key_range
   return c;
 }
 
-// Changed scores: the backward keeps one bit per 128-row query block in shared memory, and the
-// spans of the query blocks are found by a grid with the batch in y.
-int check_score_bwd(int B, int N, int d) {
+// Changed scores: the backward keeps one bit per 128-row query block in shared memory.
+int check_score_bwd(int N, int d) {
   const long long words = ((N + 127) / 128 + 31) / 32;
   const int cap = d == 64 ? fa::BwdLayout<64, 64, 64>::kScoreBitmapBytes
                   : d == 128 ? fa::BwdLayout<128, 128, 64>::kScoreBitmapBytes
                              : fa::BwdLayout<256, 128, 64>::kScoreBitmapBytes;
-  return words * 4 > cap || B > 65535 ? FA_ERR_UNSUPPORTED : FA_OK;
+  return words * 4 > cap ? FA_ERR_UNSUPPORTED : FA_OK;
 }
 
 // ---- forward
@@ -184,19 +183,21 @@ int launch_bwd_score(const BwdScoreArgs &a) {
   behind += fa::pad256(static_cast<size_t>(a.B) * p.nkb * 8);
   int *parts = reinterpret_cast<int *>(behind + plan.parts);
   const auto *ob = static_cast<const __nv_bfloat16 *>(a.o), *dob = static_cast<const __nv_bfloat16 *>(a.dout);
-  if (max_parts > 0) {
+  if (max_parts > 0 || a.score.range) {
     int4 *items = reinterpret_cast<int4 *>(behind + plan.items);
     const fa::PlanParams pp{a.score, a.B, a.N, p.nkb, a.Hq / a.Hkv, 128 / BQ, (a.N - (p.nkb - 1) * 128 + BQ - 1) / BQ,
                             a.Hkv * (D / DH), max_parts, D == 256 ? 6 : 12, blocks, parts, items};
-    const long long ctas = 1 + (rows + fa::kPlanThreads / 32 - 1) / (fa::kPlanThreads / 32);
-    fa::fa_bwd_plan_kernel<D><<<static_cast<unsigned>(ctas), fa::kPlanThreads, 0, a.s>>>(pp, ob, dob, delta, dqacc, rows);
-    p.items = items;
-    p.parts = reinterpret_cast<float *>(behind + plan.sums);
+    const unsigned ctas = static_cast<unsigned>(fa::front_blocks(max_parts > 0, a.B, p.nkb) +
+                                                (rows + fa::kPlanThreads / 32 - 1) / (fa::kPlanThreads / 32));
+    if (max_parts > 0) {
+      fa::fa_bwd_front_kernel<D, true><<<ctas, fa::kPlanThreads, 0, a.s>>>(pp, ob, dob, delta, dqacc, rows);
+      p.items = items;
+      p.parts = reinterpret_cast<float *>(behind + plan.sums);
+    } else {
+      fa::fa_bwd_front_kernel<D, false><<<ctas, fa::kPlanThreads, 0, a.s>>>(pp, ob, dob, delta, dqacc, rows);
+    }
   } else {
     fa::fa_bwd_pre_kernel<D><<<static_cast<unsigned>((rows + 7) / 8), 256, 0, a.s>>>(ob, dob, delta, dqacc, rows);
-    if (a.score.range)
-      fa::fa_score_blocks_kernel<<<dim3(static_cast<unsigned>(p.nkb), static_cast<unsigned>(a.B)), 128, 0, a.s>>>(
-          a.score, a.N, blocks);
   }
   if (a.score.range) p.blocks = blocks;
   const fa::BwdOrder order = bwd_order(a.B, a.Hkv, a.N, a.score.range ? a.N : -1, a.right);
@@ -544,7 +545,7 @@ int fa_bwd_score(const void *q, const void *k, const void *v, const void *o, con
   if (causal != 0 && causal != 1) return FA_ERR_INVALID_ARG;
   int rc = check_sizes(B, Hq, Hkv, N, d, scale);
   if (rc == FA_OK) rc = check_score_args(softcap, alibi_slopes);
-  if (rc == FA_OK) rc = check_score_bwd(B, N, d);
+  if (rc == FA_OK) rc = check_score_bwd(N, d);
   if (rc != FA_OK) return rc;
   if (!workspace || workspace_bytes < fa_bwd_score_workspace_bytes(B, Hq, Hkv, N, d)) return FA_ERR_WORKSPACE;
   const void *ptrs[] = {q, k, v, o, lse, dout, dq, dk, dv, workspace};

@@ -53,6 +53,11 @@ inline PlanLayout plan_layout(int B, int Hkv, int N, int d, int max_parts) {
   return l;
 }
 
+// Blocks of fa_bwd_front_kernel that come before those of the rows.
+__host__ __device__ inline int front_blocks(bool plan, int B, int nkb) {
+  return plan ? 1 : static_cast<int>((static_cast<long long>(B) * nkb + kPlanThreads / 32 - 1) / (kPlanThreads / 32));
+}
+
 struct PlanParams {
   ScoreCfg cfg;
   int B, N, nkb, g;     // g: query heads per K/V head
@@ -80,19 +85,8 @@ __device__ __forceinline__ void bwd_plan(const PlanParams &p) {
   const int entries = B * nkb;
   for (int e = warp; e < entries; e += warps) {
     const int b = e / nkb, qb = e - b * nkb;
-    int lo = INT_MAX, hi = 0;
-#pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      int l, h;
-      row_range(cfg, b, qb * 128 + r * 32 + lane, N, l, h);
-      if (h > l) {
-        lo = min(lo, l);
-        hi = max(hi, h);
-      }
-    }
-    lo = __reduce_min_sync(0xffffffffu, lo);
-    hi = __reduce_max_sync(0xffffffffu, hi);
-    if (lane == 0) blocks[e] = span[e] = make_int2(lo, hi);
+    const int2 r = score_block_span(cfg, b, qb, N, lane);
+    if (lane == 0) blocks[e] = span[e] = r;
   }
   __syncthreads();
   for (int e = warp; e < entries; e += warps) {
@@ -144,20 +138,30 @@ __device__ __forceinline__ void bwd_plan(const PlanParams &p) {
   }
 }
 
-// The first kernel of a backward with a plan: block 0 makes the plan, the others do what
-// fa_bwd_pre_kernel does (Delta_i = <dO_i, O_i>, a zeroed dQ accumulator), a warp per row.  (One
-// after the other they took 4 and 8 us and a launch more.)
-template <int D>
+// The first kernel of a backward with a plan or with key ranges.  The first blocks make the plan
+// (one block) or, without one, find the spans of the query blocks (a warp each); the others do
+// what fa_bwd_pre_kernel does (Delta_i = <dO_i, O_i>, a zeroed dQ accumulator), a warp per row.
+// (One after the other, plan and rows took 4 and 8 us and a launch more.)
+template <int D, bool PLAN>
 static __global__ void __launch_bounds__(kPlanThreads, 2)
-    fa_bwd_plan_kernel(const PlanParams plan, const __nv_bfloat16 *__restrict__ o, const __nv_bfloat16 *__restrict__ dout,
+    fa_bwd_front_kernel(const PlanParams plan, const __nv_bfloat16 *__restrict__ o, const __nv_bfloat16 *__restrict__ dout,
                        float *__restrict__ delta, float *__restrict__ dqacc, long long rows) {
-  if (blockIdx.x == 0) {
-    bwd_plan(plan);
+  constexpr int kWarps = kPlanThreads / 32;
+  const int lane = threadIdx.x % 32, front = front_blocks(PLAN, plan.B, plan.nkb);
+  const long long row = static_cast<long long>(static_cast<int>(blockIdx.x) - front) * kWarps + threadIdx.x / 32;
+  if (row < 0) {
+    if constexpr (PLAN) {
+      bwd_plan(plan);
+    } else {
+      const int e = static_cast<int>(blockIdx.x) * kWarps + static_cast<int>(threadIdx.x / 32), b = e / plan.nkb;
+      if (b < plan.B) {
+        const int2 r = score_block_span(plan.cfg, b, e - b * plan.nkb, plan.N, lane);
+        if (lane == 0) plan.blocks[e] = r;
+      }
+    }
     return;
   }
   constexpr int kPairs = D / 64;  // bf16 pairs per lane
-  const int lane = threadIdx.x % 32;
-  const long long row = static_cast<long long>(blockIdx.x - 1) * (kPlanThreads / 32) + threadIdx.x / 32;
   if (row >= rows) return;
   const __nv_bfloat162 *orow = reinterpret_cast<const __nv_bfloat162 *>(o + row * D) + lane * kPairs;
   const __nv_bfloat162 *drow = reinterpret_cast<const __nv_bfloat162 *>(dout + row * D) + lane * kPairs;

@@ -343,28 +343,21 @@ __device__ __forceinline__ void score_probs(uint32_t (&s)[N], const float4 *lse4
   }
 }
 
-// Smallest lo and largest hi over the rows of each 128-row query block that see a key
-// ((INT_MAX, 0) when none does): the backward's key blocks pick their query blocks by it.
-static __global__ void __launch_bounds__(128) fa_score_blocks_kernel(const ScoreCfg cfg, int N, int2 *blocks) {
-  __shared__ int red[2][4];
-  const int qb = blockIdx.x, b = blockIdx.y;
-  int lo, hi;
-  row_range(cfg, b, qb * 128 + static_cast<int>(threadIdx.x), N, lo, hi);
-  if (hi <= lo) {
-    lo = INT_MAX;
-    hi = 0;
+// Smallest lo and largest hi over the rows of a 128-row query block that see a key
+// ((INT_MAX, 0) when none does), by one warp: the backward's key blocks pick their query blocks
+// by it.
+__device__ __forceinline__ int2 score_block_span(const ScoreCfg &cfg, int b, int qb, int N, int lane) {
+  int lo = INT_MAX, hi = 0;
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    int l, h;
+    row_range(cfg, b, qb * 128 + r * 32 + lane, N, l, h);
+    if (h > l) {
+      lo = min(lo, l);
+      hi = max(hi, h);
+    }
   }
-  lo = __reduce_min_sync(0xffffffffu, lo);
-  hi = __reduce_max_sync(0xffffffffu, hi);
-  if (threadIdx.x % 32 == 0) {
-    red[0][threadIdx.x / 32] = lo;
-    red[1][threadIdx.x / 32] = hi;
-  }
-  __syncthreads();
-  if (threadIdx.x == 0)
-    blocks[static_cast<size_t>(b) * gridDim.x + qb] =
-        make_int2(min(min(red[0][0], red[0][1]), min(red[0][2], red[0][3])),
-                  max(max(red[1][0], red[1][1]), max(red[1][2], red[1][3])));
+  return make_int2(__reduce_min_sync(0xffffffffu, lo), __reduce_max_sync(0xffffffffu, hi));
 }
 
 }  // namespace fa

@@ -271,7 +271,7 @@ size_t fa_bwd_score_workspace_bytes(int B, int Hq, int Hkv, int N, int d);
  * it): arguments as fa_bwd otherwise.  dS = P (dP - Delta) (1 - tanh^2(x / softcap)).  The
  * slopes and ranges are constants: they get no gradient.  Keys that no query sees get
  * dK = dV = 0, rows without keys dQ = 0.  Every row of Q, O and dO must hold finite
- * values too, also those of queries that see no key.  Limits: B <= 65535; N below about 8 million
+ * values too, also those of queries that see no key.  Limits: N below about 8 million
  * (d = 64, 128) or 344 thousand (d = 256) rows, by the bitmap of query blocks in shared memory
  * (FA_ERR_UNSUPPORTED beyond).
  */

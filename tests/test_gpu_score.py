@@ -337,6 +337,15 @@ def test_many_and_few_key_blocks(B, Hq, Hkv, N, d, causal):
     check(q, k, v, do, causal=causal, softcap=30.0, slopes=_slopes(Hq), key_range=_mixed_ranges(B, N, N + Hq))
 
 
+def test_many_batch_entries():
+    # more entries than a grid's second dimension holds, one row each, every third without its key
+    B = 70000
+    q, k, v, do = _draw(B, 1, 1, 1, 64, seed=8)
+    r = torch.zeros(B, 1, 2, dtype=torch.int32)
+    r[:, 0, 1] = (torch.arange(B) % 3 != 0).int()
+    check(q, k, v, do, softcap=10.0, key_range=r)
+
+
 @pytest.mark.parametrize("d", [64, 128, 256])
 @pytest.mark.parametrize("softcap,q_std", [(50.0, 1.0), (8.0, 2.0), (1.0, 4.0)])
 def test_capped_ranges(d, softcap, q_std):
