@@ -98,6 +98,35 @@ __device__ __forceinline__ void score_tile_blocks(const int2 *span, int &first, 
   count = hi > 0 ? (hi - 1) / KB + 1 - first : 0;
 }
 
+// The key blocks that a CTA walks for two tiles, tile t seeing the n_t blocks from f_t on
+// (n_t = 0: none).  Rows' key ranges are free, so the two intervals may lie far apart: what lies
+// between them is left out of the walk, because the MMA role frees the ring slot of a block when
+// a tile multiplies it, and one that no tile multiplies would keep its slot for good.  Local block
+// j of the walk is key block `first` + j, and `skip` more from j = `cut` on; tile t takes part in
+// the local blocks [a[t], a[t] + n_t).
+struct TileWalk {
+  int first, count, cut, skip, a[2];
+  __host__ __device__ __forceinline__ int block(int j) const { return first + j + (j >= cut ? skip : 0); }
+};
+__host__ __device__ __forceinline__ TileWalk tile_walk(int f0, int n0, int f1, int n1) {
+  TileWalk w{0, n0 + n1, INT_MAX, 0, {0, 0}};
+  if (n0 == 0 || n1 == 0) {
+    w.first = n0 == 0 ? f1 : f0;
+    return w;
+  }
+  const bool swap = f1 < f0;  // tile 1's blocks start first
+  const int f = swap ? f1 : f0, end = f + (swap ? n1 : n0), g = swap ? f0 : f1, g_end = g + (swap ? n0 : n1);
+  w.first = f;
+  if (g > end) {
+    w.cut = end - f;
+    w.skip = g - end;
+  }
+  w.a[0] = swap ? g - f - w.skip : 0;
+  w.a[1] = swap ? 0 : g - f - w.skip;
+  w.count = (end > g_end ? end : g_end) - f - w.skip;
+  return w;
+}
+
 // Hides with -inf the scores of keys kv0 + c outside [lo, hi).
 template <int NC>
 __device__ __forceinline__ void mask_score_range(uint32_t (&s)[NC], int lo, int hi, int kv0) {
@@ -370,11 +399,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   constexpr bool GENLIKE = RANGED || SPARSE;  // rows may see no key at all
   const bool packed = GEN && p.cu_q != nullptr;
   SeqGeom sg{p.N, p.N, 0, 0, 0};
-  // Key blocks: the CTA walks the union [ulo, ulo + nu) of its tiles' ranges (contiguous:
-  // the tiles are the same rows or adjacent rows, and each range is an interval around
-  // its rows' key positions); tile t takes part in the local blocks [a[t], a[t] + nblk[t]).
+  // Key blocks: the CTA walks the union [ulo, ulo + nu) of its tiles' ranges (with a band it is
+  // contiguous: the tiles are the same rows or adjacent rows, and each range is an interval
+  // around its rows' key positions; changed scores leave a gap out, see tile_walk); tile t
+  // takes part in the local blocks [a[t], a[t] + nblk[t]).
   // A tile whose rows see no key at all has nblk = 0 and only writes O = 0, LSE = -inf.
   int a[2] = {0, 0}, nblk[2], ulo = 0, nu;
+  int cut = INT_MAX, skip = 0;  // changed scores: local blocks from `cut` on lie `skip` further on
   if constexpr (GEN) {
     if (!seq_geom(p.cu_q, p.cu_k, p.N, p.total_q, p.total_k, p.nqb * 128, INT_MAX, b, sg)) return;
     // Packed sequences: tiles that start past the sequence's end have no rows.
@@ -469,10 +500,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     int f0, f1;
     score_tile_blocks<128>(span, f0, nblk[0]);
     score_tile_blocks<128>(span + 4, f1, nblk[1]);
-    ulo = nblk[0] == 0 ? f1 : nblk[1] == 0 ? f0 : min(f0, f1);
-    a[0] = nblk[0] > 0 ? f0 - ulo : 0;
-    a[1] = nblk[1] > 0 ? f1 - ulo : 0;
-    nu = max(a[0] + nblk[0], a[1] + nblk[1]);
+    const TileWalk w = tile_walk(f0, nblk[0], f1, nblk[1]);
+    ulo = w.first;
+    nu = w.count;
+    cut = w.cut;
+    skip = w.skip;
+    a[0] = w.a[0];
+    a[1] = w.a[1];
   }
   if constexpr (SPARSE) {
     const int *hdr = reinterpret_cast<const int *>(smem + L::kOffList);
@@ -517,7 +551,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           mbar_arrive_expect_tx(bar(L::kBarKVFull + slot), L::kTileBytes);
           const CUtensorMap *m = kind ? &tm_v : &tm_k;
           int c1, c2;
-          kv_coords((SPARSE ? (blist[j] & 0x3FFF) : ulo + j) * 128, c1, c2);
+          kv_coords((SPARSE ? (blist[j] & 0x3FFF) : ulo + j + (SCORE && j >= cut ? skip : 0)) * 128, c1, c2);
 #pragma unroll
           for (int c = 0; c < L::kChunks; ++c)
             tma_load_3d(sKV + slot * L::kTileBytes + c * L::kChunkBytes, m, bar(L::kBarKVFull + slot),
@@ -727,7 +761,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     const int my_qb = t ? qb[1] : qb[0];
     const int my_h = t ? h[1] : h[0];
     const int my_n = t ? nblk[1] : nblk[0];
-    const int my_j0 = ulo + (t ? a[1] : a[0]);  // first key block of this tile
+    const int my_a = t ? a[1] : a[0];
+    const int my_j0 = ulo + my_a + (SCORE && my_a >= cut ? skip : 0);  // first key block of this tile
     const bool my_valid = t ? valid[1] : valid[0];
     const int qrow = my_qb * 128 + r;
     bool ok = my_valid;
