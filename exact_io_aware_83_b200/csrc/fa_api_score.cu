@@ -42,25 +42,45 @@ bool score_ready() {
     ok = ok && set_smem(fa::fa_bwd_q128_kernel<fa::kAttnFull, true>, fa::Q128Layout::kSmemBytes);
     ok = ok && set_smem(fa::fa_bwd_q128_kernel<fa::kAttnCausal, true>, fa::Q128Layout::kSmemBytes);
     ok = ok && set_smem(fa::fa_fwd_kernel<64, fa::kAttnScore>, fa::FwdLayout<64>::kSmemBytesScore);
+    ok = ok && set_smem(fa::fa_fwd_kernel<64, fa::kAttnScoreFar>, fa::FwdLayout<64>::kSmemBytesScore);
     ok = ok && set_smem(fa::fa_fwd_kernel<128, fa::kAttnScore>, fa::FwdLayout<128>::kSmemBytesScore);
+    ok = ok && set_smem(fa::fa_fwd_kernel<128, fa::kAttnScoreFar>, fa::FwdLayout<128>::kSmemBytesScore);
     ok = ok && regs_at_least(fa::fa_fwd_kernel<64, fa::kAttnScore>, fa::kFwdRegsLaunch);
+    ok = ok && regs_at_least(fa::fa_fwd_kernel<64, fa::kAttnScoreFar>, fa::kFwdRegsLaunch);
     ok = ok && regs_at_least(fa::fa_fwd_kernel<128, fa::kAttnScore>, fa::kFwdRegsLaunch);
+    ok = ok && regs_at_least(fa::fa_fwd_kernel<128, fa::kAttnScoreFar>, fa::kFwdRegsLaunch);
     ok = ok && set_smem(fa::fa_fwd_d256_kernel<fa::kAttnScore>, fa::FwdD256Layout::kSmemBytesScore);
+    ok = ok && set_smem(fa::fa_fwd_d256_kernel<fa::kAttnScoreFar>, fa::FwdD256Layout::kSmemBytesScore);
     ok = ok && set_smem(fa::fa_bwd_main_kernel<64, 64, 64, fa::kAttnScore>, fa::BwdLayout<64, 64, 64>::kSmemBytesScore);
+    ok = ok && set_smem(fa::fa_bwd_main_kernel<64, 64, 64, fa::kAttnScoreFar>, fa::BwdLayout<64, 64, 64>::kSmemBytesScore);
     ok = ok && set_smem(fa::fa_bwd_main_kernel<64, 64, 64, fa::kAttnScoreParts>, fa::BwdLayout<64, 64, 64>::kSmemBytesScore);
+    ok = ok && set_smem(fa::fa_bwd_main_kernel<64, 64, 64, fa::kAttnScorePartsFar>, fa::BwdLayout<64, 64, 64>::kSmemBytesScore);
     ok = ok && set_smem(fa::fa_bwd_main_kernel<128, 128, 64, fa::kAttnScore>, fa::BwdLayout<128, 128, 64>::kSmemBytesScore);
+    ok = ok && set_smem(fa::fa_bwd_main_kernel<128, 128, 64, fa::kAttnScoreFar>, fa::BwdLayout<128, 128, 64>::kSmemBytesScore);
     ok = ok && set_smem(fa::fa_bwd_main_kernel<128, 128, 64, fa::kAttnScoreParts>, fa::BwdLayout<128, 128, 64>::kSmemBytesScore);
+    ok = ok && set_smem(fa::fa_bwd_main_kernel<128, 128, 64, fa::kAttnScorePartsFar>, fa::BwdLayout<128, 128, 64>::kSmemBytesScore);
     ok = ok && set_smem(fa::fa_bwd_main_kernel<256, 128, 64, fa::kAttnScore>, fa::BwdLayout<256, 128, 64>::kSmemBytesScore);
+    ok = ok && set_smem(fa::fa_bwd_main_kernel<256, 128, 64, fa::kAttnScoreFar>, fa::BwdLayout<256, 128, 64>::kSmemBytesScore);
     ok = ok && set_smem(fa::fa_bwd_main_kernel<256, 128, 64, fa::kAttnScoreParts>, fa::BwdLayout<256, 128, 64>::kSmemBytesScore);
+    ok = ok && set_smem(fa::fa_bwd_main_kernel<256, 128, 64, fa::kAttnScorePartsFar>, fa::BwdLayout<256, 128, 64>::kSmemBytesScore);
     ok = ok && set_smem(fa::fa_decode_kernel<64, 32, true>, fa::DecodeLayout<64, 32>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kernel<64, 32, true, true>, fa::DecodeLayout<64, 32>::kSmemBytes);
     ok = ok && set_smem(fa::fa_decode_kernel<64, 64, true>, fa::DecodeLayout<64, 64>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kernel<64, 64, true, true>, fa::DecodeLayout<64, 64>::kSmemBytes);
     ok = ok && set_smem(fa::fa_decode_kernel<64, 128, true>, fa::DecodeLayout<64, 128>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kernel<64, 128, true, true>, fa::DecodeLayout<64, 128>::kSmemBytes);
     ok = ok && set_smem(fa::fa_decode_kernel<128, 32, true>, fa::DecodeLayout<128, 32>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kernel<128, 32, true, true>, fa::DecodeLayout<128, 32>::kSmemBytes);
     ok = ok && set_smem(fa::fa_decode_kernel<128, 64, true>, fa::DecodeLayout<128, 64>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kernel<128, 64, true, true>, fa::DecodeLayout<128, 64>::kSmemBytes);
     ok = ok && set_smem(fa::fa_decode_kernel<128, 128, true>, fa::DecodeLayout<128, 128>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kernel<128, 128, true, true>, fa::DecodeLayout<128, 128>::kSmemBytes);
     ok = ok && set_smem(fa::fa_decode_kernel<256, 16, true>, fa::DecodeLayout<256, 16>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kernel<256, 16, true, true>, fa::DecodeLayout<256, 16>::kSmemBytes);
     ok = ok && set_smem(fa::fa_decode_kernel<256, 32, true>, fa::DecodeLayout<256, 32>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kernel<256, 32, true, true>, fa::DecodeLayout<256, 32>::kSmemBytes);
     ok = ok && set_smem(fa::fa_decode_kernel<256, 64, true>, fa::DecodeLayout<256, 64>::kSmemBytes);
+    ok = ok && set_smem(fa::fa_decode_kernel<256, 64, true, true>, fa::DecodeLayout<256, 64>::kSmemBytes);
     ok = ok && set_smem(fa::fa_decode_kv4_kernel<64, 1, false>, fa::KV4Layout<64, 1>::kSmemBytes);
     ok = ok && set_smem(fa::fa_decode_kv4_kernel<64, 1, true>, fa::KV4Layout<64, 1>::kSmemBytes);
     ok = ok && set_smem(fa::fa_decode_kv4_kernel<64, 2, false>, fa::KV4Layout<64, 2>::kSmemBytes);
@@ -129,15 +149,23 @@ int check_score_bwd(int N, int d) {
 
 // ---- forward
 
+// A cap beyond which a score needs the other form of the tanh (fa_score.cuh).
+bool far_cap(const fa::ScoreCfg &c) { return c.cap_log2 > fa::kCapNear * fa::kLog2e; }
+
+template <int D, int MODE>
+void launch_fwd_mode(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const CUtensorMap &to,
+                     const fa::FwdParams &p, unsigned units, cudaStream_t s) {
+  if constexpr (D == 256)
+    fa::fa_fwd_d256_kernel<MODE><<<units, fa::kFwdD256Threads, fa::FwdD256Layout::kSmemBytesScore, s>>>(tq, tk, tv, to, p);
+  else
+    fa::fa_fwd_kernel<D, MODE><<<units, fa::kFwdThreads, fa::FwdLayout<D>::kSmemBytesScore, s>>>(tq, tk, tv, to, p);
+}
+
 template <int D>
 void launch_fwd_score(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const CUtensorMap &to,
                       const fa::FwdParams &p, unsigned units, cudaStream_t s) {
-  if constexpr (D == 256)
-    fa::fa_fwd_d256_kernel<fa::kAttnScore><<<units, fa::kFwdD256Threads, fa::FwdD256Layout::kSmemBytesScore, s>>>(
-        tq, tk, tv, to, p);
-  else
-    fa::fa_fwd_kernel<D, fa::kAttnScore><<<units, fa::kFwdThreads, fa::FwdLayout<D>::kSmemBytesScore, s>>>(tq, tk, tv,
-                                                                                                        to, p);
+  if (far_cap(p.score)) launch_fwd_mode<D, fa::kAttnScoreFar>(tq, tk, tv, to, p, units, s);
+  else launch_fwd_mode<D, fa::kAttnScore>(tq, tk, tv, to, p, units, s);
 }
 
 // ---- backward
@@ -209,8 +237,9 @@ int launch_bwd_score(const BwdScoreArgs &a) {
   // scores do: causal B = 2, Hq = 32, Hkv = 8, N = 4096 915 us against 978 with slopes, 1359
   // against 1454 with both.  A cap alone fits the 64-query steps better as long as most scores
   // stay in its shorter polynomials (1089 against 1055 us at cap 50 and standard normal q and k;
-  // 1152 against 1177 at cap 5).
-  const bool wide = a.score.slopes && !a.score.range && max_parts == 0 && D == 128 && a.N >= fa::kQ128MinN;
+  // 1152 against 1177 at cap 5).  A cap beyond kCapNear takes those too.
+  const bool far = far_cap(a.score);
+  const bool wide = a.score.slopes && !far && !a.score.range && max_parts == 0 && D == 128 && a.N >= fa::kQ128MinN;
   bool launched = true;
   const int tslot = timer_start(1, a.s);
   if (wide) {
@@ -227,8 +256,12 @@ int launch_bwd_score(const BwdScoreArgs &a) {
                fa::bwd_map(e, &tdk, a.dk, false, D, a.N, hkv, 64, 128) && fa::bwd_map(e, &tdv, a.dv, false, D, a.N, hkv, 64, 128) &&
                fa::bwd_map(e, &tdq, dqacc, true, D, a.N, hq, L::kDQCols, BQ);
     const unsigned grid = static_cast<unsigned>(a.B) * a.Hkv * p.nkb * (D / DH) * (max_parts > 0 ? max_parts : 1);
-    if (launched && max_parts > 0)
+    if (launched && max_parts > 0 && far)
+      fa::bwd_launch_main<D, DH, BQ, fa::kAttnScorePartsFar>(tq, tk, tv, tdo, tdk, tdv, tdq, p, grid, a.s);
+    else if (launched && max_parts > 0)
       fa::bwd_launch_main<D, DH, BQ, fa::kAttnScoreParts>(tq, tk, tv, tdo, tdk, tdv, tdq, p, grid, a.s);
+    else if (launched && far)
+      fa::bwd_launch_main<D, DH, BQ, fa::kAttnScoreFar>(tq, tk, tv, tdo, tdk, tdv, tdq, p, grid, a.s);
     else if (launched)
       fa::bwd_launch_main<D, DH, BQ, fa::kAttnScore>(tq, tk, tv, tdo, tdk, tdv, tdq, p, grid, a.s);
   }
@@ -253,7 +286,9 @@ int launch_bwd_score(const BwdScoreArgs &a) {
 template <int D, int RP>
 void launch_decode(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const fa::DecodeParams &p,
                    unsigned grid, cudaStream_t s) {
-  fa::fa_decode_kernel<D, RP, true><<<grid, fa::kDecodeThreads, fa::DecodeLayout<D, RP>::kSmemBytes, s>>>(tq, tk, tv, p);
+  constexpr int smem = fa::DecodeLayout<D, RP>::kSmemBytes;
+  if (far_cap(p.score)) fa::fa_decode_kernel<D, RP, true, true><<<grid, fa::kDecodeThreads, smem, s>>>(tq, tk, tv, p);
+  else fa::fa_decode_kernel<D, RP, true><<<grid, fa::kDecodeThreads, smem, s>>>(tq, tk, tv, p);
 }
 
 template <int D>

@@ -119,10 +119,10 @@ struct BwdParams {
   const uint8_t *bmask;   // block-sparse: [B, Hq, nkb, nkb] 0/1 over 128 x 128 blocks
   int tsz;                // unit order: key-block levels per tier (see unit_order)
   int tail;               // unit order: heads taken level by level at the end
-  ScoreCfg score;         // changed scores (kAttnScore, kAttnScoreParts only)
+  ScoreCfg score;         // changed scores (kAttnScore.. only)
   const int2 *blocks;     // changed scores with key ranges: [B, nkb] span of each 128-row query block
   const int4 *items;      // changed scores: (key block, batch entry, part, parts) in launch order
-                          //   (kAttnScoreParts only, see fa_bwd_plan.cuh)
+                          //   (kAttnScoreParts.. only, see fa_bwd_plan.cuh)
   float *parts;           // dK, dV of key blocks in several parts: [part][B, Hkv][nkb][dV | dK][D / 4][128][4] fp32
 };
 
@@ -312,9 +312,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   // mask) first
   const int half = static_cast<int>(blockIdx.x) % kHalves;
   int head, kb;
-  constexpr bool SCORE = MODE == kAttnScore || MODE == kAttnScoreParts;
+  constexpr bool PARTS = MODE == kAttnScoreParts || MODE == kAttnScorePartsFar;
+  constexpr bool FAR = MODE == kAttnScoreFar || MODE == kAttnScorePartsFar;
+  constexpr bool SCORE = MODE >= kAttnScore;
   int part = 0, parts = 1;  // this CTA takes part `part` of `parts` of the unit's steps
-  if constexpr (MODE == kAttnScoreParts) {
+  if constexpr (PARTS) {
     const int u = static_cast<int>(blockIdx.x) / kHalves, item = u / p.Hkv;
     const int4 it = p.items[item];
     if (it.w == 0) return;  // behind the last part
@@ -454,7 +456,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
   // Block-sparse: each role's cursor, moved once per step before (h, q0) are used.
   SparseSteps cur;
   if constexpr (LISTED) cur.init(spbits, spW, g, p.nkb, kSub, spSubLast, SCORE ? 0 : spW);
-  if constexpr (MODE == kAttnScoreParts) {
+  if constexpr (PARTS) {
     if (parts > 1) {
       const int first = static_cast<int>(static_cast<long long>(T) * part / parts);
       const int end = static_cast<int>(static_cast<long long>(T) * (part + 1) / parts);
@@ -744,7 +746,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
           const bool part = sc_flag[st] == 0;  // some row of the step does not see the whole key block
           const int4 *lo4 = reinterpret_cast<const int4 *>(sc_range + (st * 2) * BQ + c0);
           const int4 *hi4 = reinterpret_cast<const int4 *>(sc_range + (st * 2 + 1) * BQ + c0);
-          score_probs<HC>(rr, lse4, p.score, p.sl2, slope2, kv, q0, side,
+          score_probs<HC, FAR>(rr, lse4, p.score, p.sl2, slope2, kv, q0, side,
                           [&](int c, const float (&p4)[4], const float (&g4)[4]) {
 #pragma unroll
                             for (int k = 0; k < 4; ++k) pr[c + k] = g4[k];
@@ -904,7 +906,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) o[i] = 0u;  // no query sees this block
         }
-        if constexpr (MODE == kAttnScoreParts) {
+        if constexpr (PARTS) {
           if (parts > 1) {  // summed, scaled and rounded by fa_bwd_join_kernel
             // (four columns of all 128 rows next to one another: 512 bytes a warp and store)
             uint4 *dst = reinterpret_cast<uint4 *>(p.parts) +
@@ -930,7 +932,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             *reinterpret_cast<uint4 *>(drow + cc * 32 + uu * 8) = make_uint4(w[0], w[1], w[2], w[3]);
         }
       }
-      if (!direct && !(MODE == kAttnScoreParts && parts > 1)) {
+      if (!direct && !(PARTS && parts > 1)) {
         fence_proxy_async_smem();
         named_bar_sync(1, 256);
         if (threadIdx.x == 0) {

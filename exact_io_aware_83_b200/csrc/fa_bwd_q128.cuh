@@ -360,7 +360,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         for (int h = 0; h < 2; ++h) {
           uint32_t rr[32], pk32[16];
           tmem_ld_x32(tS + 32 * h, rr);
-          score_probs<32>(rr, lse4 + 8 * h, p.score, sl2, slope2, kv, q0 + 32 * h, side,
+          score_probs<32, false>(rr, lse4 + 8 * h, p.score, sl2, slope2, kv, q0 + 32 * h, side,
                           [&](int c, const float (&p4)[4], const float (&g4)[4]) {
                             pg[16 * h + c / 2] = pack_f16x2(g4[0] * kGradUp, g4[1] * kGradUp);
                             pg[16 * h + c / 2 + 1] = pack_f16x2(g4[2] * kGradUp, g4[3] * kGradUp);

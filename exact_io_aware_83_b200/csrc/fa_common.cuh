@@ -111,9 +111,9 @@ struct DropCfg {
 // causal mask); only enabled blocks are visited.
 // kAttnScore: dense layout with changed scores (a tanh cap, a distance bias, a key range per
 // query row; see fa_score.cuh); kAttnScoreParts: the backward of it with the key blocks in
-// parts (fa_bwd_plan.cuh).
+// parts (fa_bwd_plan.cuh); ..Far: the same for a cap beyond kCapNear.
 constexpr int kAttnFull = 0, kAttnCausal = 1, kAttnGeneral = 2, kAttnSparse = 3, kAttnScore = 4,
-              kAttnScoreParts = 5;
+              kAttnScoreParts = 5, kAttnScoreFar = 6, kAttnScorePartsFar = 7;
 
 // Order of the work units of a grid: `heads` rows of `levels` units each, level 0 the
 // heaviest (the most key blocks under a causal mask).  Levels are cut into tiers of `tsz`

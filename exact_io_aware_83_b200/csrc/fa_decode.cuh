@@ -137,7 +137,7 @@ __device__ __forceinline__ void st_shared_u16(uint32_t addr, uint16_t v) {
   asm volatile("st.shared.u16 [%0], %1;" ::"r"(addr), "h"(v) : "memory");
 }
 
-template <int D, int RP, bool SCORE = false>
+template <int D, int RP, bool SCORE = false, bool FAR = false>  // FAR: a cap beyond kCapNear
 __global__ void __launch_bounds__(kDecodeThreads, DecodeLayout<D, RP>::kCtasPerSM)
     fa_decode_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                      const __grid_constant__ CUtensorMap tm_v, const DecodeParams p) {
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kDecodeThreads, DecodeLayout<D, RP>::kCtasPerS
         float none[1];
         ScoreCfg capped = p.score;
         capped.slopes = nullptr;
-        score_log2<CW, false, false>(sc, none, capped, p.sl2, 0.f, 0, 0, 0);
+        score_log2<CW, false, FAR, false>(sc, none, capped, p.sl2, 0.f, 0, 0, 0);
         if (p.score.slopes) {
           // column c is token t = c mod Nq of query head c / Nq of the group
           const int grp = p.R / p.Nq;

@@ -135,13 +135,12 @@ __device__ __forceinline__ LineCursor<KB> line_cursor(const LineParams &p, const
   return c;
 }
 
-// The score in log2 units from x = scale q . k: capped, y = cap tanh(x / cap) log2(e).
-// tanh(u) = sign(u) (1 - w) / (1 + w), w = exp(-2 |u|): no cancellation that matters, the
-// absolute error stays below 2^-22 for every u.
-__device__ __forceinline__ float softcap_log2(float x, float inv_cap2, float cap_log2) {
-  // inv_cap2 = 2 log2(e) / cap
-  const float w = ex2_approx(-fabsf(x) * inv_cap2);
-  return copysignf(cap_log2 * __fdividef(1.f - w, 1.f + w), x);
+// The score in log2 units from x = scale q . k: capped, y = cap tanh(x / cap) log2(e).  FAR: the
+// cap may lie beyond kCapNear.
+template <bool FAR>
+__device__ __forceinline__ float softcap_log2(float x, float inv_cap, float cap_log2) {
+  float grad;
+  return cap_log2 * tanh_any<FAR>(x * inv_cap, grad);
 }
 
 __device__ __forceinline__ uint32_t movmatrix_trans(uint32_t a) {

@@ -126,7 +126,7 @@ __global__ void __launch_bounds__(DecScoreLayout<D, NT>::W * 32, 1)
     for (int i = 0; i < min(S, total); ++i) issue();
 
   const int grp = p.R / p.Nq;  // query heads per K/V head
-  const float inv_cap2 = p.softcap > 0.f ? 2.f * kLog2e / p.softcap : 0.f;
+  const float inv_cap = p.softcap > 0.f ? 1.f / p.softcap : 0.f;
   const float cap_log2 = p.softcap * kLog2e;
   const float raw = p.softcap > 0.f ? p.scale : p.sl2;
   // This lane's piece of K: 16 bytes of key g (and g + 8), and its row of V for ldmatrix.
@@ -212,7 +212,7 @@ __global__ void __launch_bounds__(DecScoreLayout<D, NT>::W * 32, 1)
           for (int e = 0; e < 4; ++e) {
             const int key = kb + g + 8 * (e / 2);
             float v = y[nt][e] * raw;
-            if (p.softcap > 0.f) v = softcap_log2(v, inv_cap2, cap_log2);
+            if (p.softcap > 0.f) v = softcap_log2<true>(v, inv_cap, cap_log2);
             v = fmaf(-slope2[nt][e & 1], fabsf(static_cast<float>(rpos[nt][e & 1] - key)), v);
             y[nt][e] = (key >= len || (p.causal && key > rpos[nt][e & 1])) ? -INFINITY : v;
           }

@@ -57,7 +57,7 @@ struct FwdParams {
   const uint8_t *bmask;   // block-sparse: [B, Hq, nqb, nqb] 0/1 over 128 x 128 blocks
   int tsz;                // unit order: levels per tier (see unit_order)
   int tail;               // unit order: heads taken level by level at the end
-  ScoreCfg score;         // changed scores (kAttnScore only)
+  ScoreCfg score;         // changed scores (kAttnScore, kAttnScoreFar only)
 };
 
 // Blocks of KB keys [lo, hi] that some row q0 .. min(q0 + 127, Lq - 1) of a query tile can
@@ -394,7 +394,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
   const int kvh = h[0] / g;
   constexpr bool GEN = MODE == kAttnGeneral;
   constexpr bool SPARSE = MODE == kAttnSparse;
-  constexpr bool SCORE = MODE == kAttnScore;
+  constexpr bool SCORE = MODE == kAttnScore || MODE == kAttnScoreFar;
   constexpr bool RANGED = GEN || SCORE;    // each tile has a key-block range of its own
   constexpr bool GENLIKE = RANGED || SPARSE;  // rows may see no key at all
   const bool packed = GEN && p.cu_q != nullptr;
@@ -831,7 +831,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
           if (changed) {
             const int side = p.score.causal || kv0 + 127 <= my_qb * 128 ? -1 : (kv0 >= my_qb * 128 + 127 ? 1 : 0);
             float none[1];
-            score_log2<128, false>(s, none, p.score, p.sl2, slope2, qrow, kv0, side);
+            score_log2<128, false, MODE == kAttnScoreFar>(s, none, p.score, p.sl2, slope2, qrow, kv0, side);
           }
           if (hides) mask_score_range<128>(s, row_lo, row_hi, kv0);
         }

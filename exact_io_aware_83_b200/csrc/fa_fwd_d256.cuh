@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kFwdD256Threads, 1)
   const int kvh = h / (p.Hq / p.Hkv);
   constexpr bool GEN = MODE == kAttnGeneral;
   constexpr bool SPARSE = MODE == kAttnSparse;
-  constexpr bool SCORE = MODE == kAttnScore;
+  constexpr bool SCORE = MODE == kAttnScore || MODE == kAttnScoreFar;
   constexpr bool RANGED = GEN || SCORE;
   constexpr bool GENLIKE = RANGED || SPARSE;  // rows may see no key at all
   const bool packed = GEN && p.cu_q != nullptr;
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kFwdD256Threads, 1)
           if (changed) {
             const int side = p.score.causal || kv0 + 63 <= qb * 128 ? -1 : (kv0 >= qb * 128 + 127 ? 1 : 0);
             float none[1];
-            score_log2<64, false>(s, none, p.score, p.sl2, slope2, qrow, kv0, side);
+            score_log2<64, false, MODE == kAttnScoreFar>(s, none, p.score, p.sl2, slope2, qrow, kv0, side);
           }
           if (hides) mask_score_range<64>(s, row_lo, row_hi, kv0);
         }

@@ -400,7 +400,7 @@ __global__ void __launch_bounds__(kKV4Warps * 32, KV4Layout<D, NT>::kCtas)
   asm volatile("mov.b32 %0, 0x64006400;" : "=r"(magic0));
   asm volatile("mov.b32 %0, 0x54005400;" : "=r"(magic1));
   const int grp = p.R / p.Nq;  // query heads per K/V head
-  const float inv_cap2 = p.softcap > 0.f ? 2.f * kLog2e / p.softcap : 0.f;
+  const float inv_cap = p.softcap > 0.f ? 1.f / p.softcap : 0.f;
   const float cap_log2 = p.softcap * kLog2e;
   const int ka = kv4_key_of_row(g);  // key of row g; row g + 8 is ka + 8
   const int vgroup = (g * VW) / 4;   // group of this lane's V channels
@@ -591,9 +591,25 @@ __global__ void __launch_bounds__(kKV4Warps * 32, KV4Layout<D, NT>::kCtas)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
+            for (int e = 0; e < 4; ++e) y[st][nt][e] *= raw[nt][e & 1];
+        auto cap_all = [&](auto far) {
+#pragma unroll
+          for (int st = 0; st < 2; ++st)
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                y[st][nt][e] = softcap_log2<decltype(far)::value>(y[st][nt][e], inv_cap, cap_log2);
+        };
+        if (p.softcap > kCapNear) cap_all(Flag<true>{});
+        else if (p.softcap > 0.f) cap_all(Flag<false>{});
+#pragma unroll
+        for (int st = 0; st < 2; ++st)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
             for (int e = 0; e < 4; ++e) {
-              float v = y[st][nt][e] * raw[nt][e & 1];
-              if (p.softcap > 0.f) v = softcap_log2(v, inv_cap2, cap_log2);
+              const float v = y[st][nt][e];
               const int key = kb + 16 * st + ka + 8 * (e / 2);
               y[st][nt][e] = fmaf(-slope2[nt][e & 1], fabsf(static_cast<float>(rpos[nt][e & 1] - key)), v);
             }

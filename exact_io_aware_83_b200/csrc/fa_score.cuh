@@ -16,9 +16,16 @@
 //    (5.9e-7).  In blocks without hidden keys and without a bias, scale, cap and log2(e) are
 //    folded into the coefficients and the softmax's offset into the last product, so that a
 //    capped pair of scores costs five or seven packed operations where a plain one costs one;
-//  * beyond: t = sign(u) (1 - w) / (1 + w), w = 2^(-2 log2(e) |u|): two MUFU operations; the
-//    absolute error stays below 2^-21, whatever u.  1 - t^2 is then 4 w / (1 + w)^2, which
-//    keeps its relative accuracy where t is near 1 (1 - t t would be all rounding there).
+//  * beyond: t = sign(u) (1 - w) / (1 + w), w = 2^(-2 log2(e) |u|): two MUFU operations.
+//    1 - t^2 is then 4 w / (1 + w)^2, which keeps its relative accuracy where t is near 1
+//    (1 - t t would be all rounding there).  Near u = 0 the difference 1 - w cancels: t is off by
+//    up to 2^-22 and the score by cap 2^-22, however small it is - 1.5e-5 at a cap of 64, less than
+//    the products' own fp32 error, but 0.2 at 1e6.  So beyond a cap of 64 (kCapNear) each u up to
+//    0.5 takes the polynomial of degree 3 instead: a relative error of 2^-20 or less for every u.
+//    Up to 64 that is left out, by variants of the kernels that choose between the forms: taken
+//    always it costs 7-13% of the saturated forward (cap 1, B = 2, Hq = 32, Hkv = 8, N = 4096,
+//    d = 128: 655 against 740 us), and as a branch in one kernel 7%.  (One rational function for
+//    every u, with one MUFU operation, measured 720.)
 #pragma once
 
 #include "fa_common.cuh"
@@ -38,14 +45,22 @@ struct ScoreCfg {
 };
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kTanhPolyMax = 1.f;
+constexpr float kTanhPolyMax = 1.f, kTanhPoly3Max = 0.5f;
+constexpr float kCapNear = 64.f;
 __host__ __device__ constexpr float tanh_coef(int i) {
   return i == 0 ? 0.9999994136f : i == 1 ? -0.3332904238f : i == 2 ? 0.1328143387f : i == 3 ? -0.05160567377f : i == 4 ? 0.01674311481f : -0.003067060224f;
+}
+__host__ __device__ constexpr float tanh3_coef(int i) {
+  return i == 0 ? 0.9999994557708327f : i == 1 ? -0.33326317935183836f : i == 2 ? 0.13190296595162188f : -0.044402225913669886f;
 }
 
 template <int D>
 struct Degree {
   static constexpr int value = D;
+};
+template <bool B>
+struct Flag {
+  static constexpr bool value = B;
 };
 
 // tanh of a pair, |u| <= kTanhPolyMax.
@@ -57,12 +72,17 @@ __device__ __forceinline__ uint64_t f2_tanh_poly(uint64_t u) {
   return f2_mul(q, u);
 }
 
-// tanh of any u, and 1 - tanh^2.
+// tanh of any u, and 1 - tanh^2.  FAR: accurate near u = 0 too, relative to tanh.
+template <bool FAR>
 __device__ __forceinline__ float tanh_any(float u, float &grad) {
   const float w = ex2_approx(fabsf(u) * (-2.f * kLog2e));
   const float r = __fdividef(1.f, 1.f + w);
   grad = 4.f * w * r * r;
-  return copysignf((1.f - w) * r, u);
+  const float t = copysignf((1.f - w) * r, u);
+  if constexpr (!FAR) return t;
+  const float z = u * u;
+  const float p = fmaf(fmaf(fmaf(tanh3_coef(3), z, tanh3_coef(2)), z, tanh3_coef(1)), z, tanh3_coef(0)) * u;
+  return fabsf(u) <= kTanhPoly3Max ? p : t;
 }
 
 // P(r^2) of the folded polynomial of degree DEG for a pair of raw products r.
@@ -165,8 +185,9 @@ __device__ __forceinline__ float row_absmax(const uint32_t (&s)[N]) {
 // Turns the raw products s[c] = q . k of one fixed index (row or key) `at` with N consecutive
 // others `first` + c into scores in log2 units, in place.  `side`: -1 when every other index
 // is <= at, +1 when every one is >= at, 0 otherwise (the same for the whole warp).  With GRAD
-// and a cap, grad[c] = 1 - tanh^2.  POLY = false leaves the polynomial form out.
-template <int N, bool GRAD, bool POLY = true>
+// and a cap, grad[c] = 1 - tanh^2.  FAR: the cap may lie beyond kCapNear.  POLY = false leaves the
+// polynomial for all of them out.
+template <int N, bool GRAD, bool FAR, bool POLY = true>
 __device__ __forceinline__ void score_log2(uint32_t (&s)[N], float (&grad)[GRAD ? N : 1], const ScoreCfg &cfg,
                                            float sl2, float slope2, int at, int first, int side) {
   if (cfg.cap_in > 0.f) {
@@ -189,7 +210,7 @@ __device__ __forceinline__ void score_log2(uint32_t (&s)[N], float (&grad)[GRAD 
 #pragma unroll
       for (int c = 0; c < N; ++c) {
         float slope;
-        s[c] = __float_as_uint(cfg.cap_log2 * tanh_any(__uint_as_float(s[c]) * cfg.cap_in, slope));
+        s[c] = __float_as_uint(cfg.cap_log2 * tanh_any<FAR>(__uint_as_float(s[c]) * cfg.cap_in, slope));
         if constexpr (GRAD) grad[c] = slope;
       }
     }
@@ -234,7 +255,7 @@ __device__ __forceinline__ void score_log2(uint32_t (&s)[N], float (&grad)[GRAD 
 
 // P = 2^(score - lse) of N raw products of one fixed index with N others whose LSE (log2 units)
 // is lse4, as in the backward: calls out(c, p, g) for each four of them, g = P (1 - tanh^2).
-template <int N, typename Out>
+template <int N, bool FAR, typename Out>
 __device__ __forceinline__ void score_probs(uint32_t (&s)[N], const float4 *lse4, const ScoreCfg &cfg, float sl2,
                                             float slope2, int at, int first, int side, Out out) {
   if (cfg.cap_in <= 0.f && !cfg.slopes) {
@@ -326,7 +347,7 @@ __device__ __forceinline__ void score_probs(uint32_t (&s)[N], const float4 *lse4
     for (int h = 0; h < N / 16; ++h) {
       uint32_t (&s16)[16] = *reinterpret_cast<uint32_t(*)[16]>(&s[16 * h]);
       float grad[16];
-      score_log2<16, true>(s16, grad, cfg, sl2, slope2, at, first + 16 * h, side);
+      score_log2<16, true, FAR>(s16, grad, cfg, sl2, slope2, at, first + 16 * h, side);
 #pragma unroll
       for (int c = 0; c < 16; c += 4) {
         const float4 l = lse4[4 * h + c / 4];

@@ -3,11 +3,15 @@ references: key ranges that lie far apart or at the ends of int32, caps from the
 number to the largest.  Bounds as in test_gpu_score.py unless a test gives its own."""
 import math
 
+import numpy as np
 import pytest
 import torch
 
+import kv4_reference
+import score_reference as ref
 from exact_io_aware_83_b200 import fa
-from test_gpu_score import _draw, _slopes, check
+from test_gpu_kv4 import _cache_of, _f64
+from test_gpu_score import _decode_ref, _draw, _guarded, _slopes, check
 
 pytestmark = pytest.mark.gpu
 
@@ -30,3 +34,109 @@ def test_neighbouring_tiles_that_see_far_apart_keys(d, near, far, Hq, Hkv):
     q, k, v, do = _draw(2, Hq, Hkv, N, d, seed=d + Hq + near[0] + far[0])
     check(q, k, v, do, key_range=r)
     check(q, k, v, do, key_range=r, softcap=20.0, slopes=_slopes(Hq))
+
+
+# Caps far above the scores.  The score c tanh(x / c) is then nearly x, whatever c, so nothing in
+# these bounds may grow with the cap: a score s is off by the tanh's 5.4e-7 |s| and eight
+# fp32 roundings (of 1 / c, c log2(e) and the products: 2^-24 |s| each), below 2^-19.5 |s| in all,
+# on top of the product's 2^-17 A (A_i = scale max_j sum_c |q_c k_c|, which also bounds |s|).
+
+LARGE = 2.0 ** -17 + 2.0 ** -19.5
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("Hq,Hkv,Nq,Nk,lens", [(8, 2, 1, 5000, [5000, 1234]), (12, 1, 5, 700, [700, 129]),
+                                               (2, 2, 3, 400, [400, 2])])
+@pytest.mark.parametrize("softcap", [1e4, 1e6, 1e9])
+def test_decode_with_caps_above_every_score(d, Hq, Hkv, Nq, Nk, lens, softcap):
+    g = torch.Generator().manual_seed(Hq * 100 + Nq + d)
+    q = (torch.randn(2, Hq, Nq, d, generator=g) * 3).to(torch.bfloat16)
+    k, v = (torch.randn(2, Hkv, Nk, d, generator=g).to(torch.bfloat16) for _ in range(2))
+    scale = 1 / math.sqrt(d)
+    o, lse = fa.decode(q.cuda(), k.cuda(), v.cuda(), seqlens_k=torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                       causal=True, softcap=softcap)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status(None) == fa.FA_OK
+    o_r, lse_r, av, size = _decode_ref(q, k, v, lens, True, scale, softcap, None)
+    delta = LARGE * size
+    o, lse = _f64(o), _f64(lse)
+    live = np.isfinite(lse_r)
+    assert np.array_equal(np.isneginf(lse), ~live) and (o[~live] == 0).all()
+    off = np.abs(lse[live] - lse_r[live]) - (delta[live] + 2.0 ** -20 * (1 + np.abs(lse_r[live])))
+    assert (off <= 0).all(), float(off.max())
+    # Up to 16 rows a K/V head (8 at d = 256) P is the sum of two bf16 numbers, 2^-16 off, and an
+    # accumulator takes at most 2 * 5000 / 64 = 157 products, each 2^-22 of what has been added up:
+    # 2^-14 with the sum of P; with more rows P is rounded to bf16, in the product and in its sum.
+    bits = -14 if Hq // Hkv * Nq <= (8 if d == 256 else 16) else -6.9
+    tol = 2.0 ** -8 * np.abs(o_r) + (2.0 ** bits + 2 * delta[..., None]) * av + 2.0 ** -30
+    assert (np.abs(o - o_r) <= tol).all(), float((np.abs(o - o_r) / tol).max())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("Hq,Hkv,Nq", [(8, 2, 1), (12, 1, 5)])
+@pytest.mark.parametrize("softcap", [1e4, 1e6, 1e9])
+def test_decode_kv4_with_caps_above_every_score(d, Hq, Hkv, Nq, softcap):
+    # bounds of test_gpu_kv4.py, with |s| <= A in the place of the cap
+    n, lens, scale = 700, [700, 401], 1 / math.sqrt(d)
+    g = torch.Generator().manual_seed(Hq + d)
+    q = (torch.randn(2, Hq, Nq, d, generator=g) * 3).to(torch.bfloat16)
+    k, v = (torch.randn(2, Hkv, n, d, generator=g).to(torch.bfloat16) for _ in range(2))
+    o, lse = fa.decode_kv4(q.cuda(), _cache_of(k, v, 704), softcap=softcap, causal=True,
+                           seqlens_k=torch.tensor(lens, dtype=torch.int32, device="cuda"))
+    torch.cuda.synchronize()
+    assert fa.fa_device_status(None) == fa.FA_OK
+    pk, pv = kv4_reference.quantise(_f64(k)), kv4_reference.quantise(_f64(v))
+    big = np.repeat(np.abs(pk[2]) + 15 * pk[1], 32, -1)
+    v64 = kv4_reference.values(*pv)
+    o_r, lse_r, av, _ = kv4_reference.decode(_f64(q), kv4_reference.values(*pk), v64, lens, True, scale, softcap)
+    A = scale * np.einsum("bhtc,bhc->bht", np.abs(_f64(q)), np.repeat(big.max(2), Hq // Hkv, 1))
+    delta = LARGE * A + 2.0 ** -20
+    tol = (2.0 ** -8 * np.abs(o_r) + (2.0 ** -10 + 2 * delta[..., None] + 2.0 ** -18) * av
+           + 2.0 ** -24 * np.abs(v64).max())
+    assert (np.abs(_f64(lse) - lse_r) <= delta + 2.0 ** -20 * (1 + np.abs(lse_r))).all(), \
+        float(np.abs(_f64(lse) - lse_r).max())
+    assert (np.abs(_f64(o) - o_r) <= tol).all(), float((np.abs(_f64(o) - o_r) / tol).max())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("softcap", [64.0, 100.0, 1e5, 1e7])
+@pytest.mark.parametrize("causal,slopes", [(False, False), (True, False), (True, True)])
+def test_small_scores_beside_rows_beyond_the_cap(d, softcap, causal, slopes):
+    # every other query is so large that all its scores are at the cap: the rows between them, which
+    # share their warps, must not lose what lies below the cap's own resolution
+    B, Hq, N, scale = 1, 2, 260, 1 / math.sqrt(d)
+    q, k, v, do = _draw(B, Hq, 1, N, d, seed=d + int(math.log2(softcap)), q_std=2.0)
+    q[:, :, 1::2] *= 2.0 ** 30
+    sl = _slopes(Hq) if slopes else None
+    kw = dict(causal=causal, softcap=softcap)
+    gpu = dict(kw, alibi_slopes=None if sl is None else sl.cuda())
+    qd, kd, vd, dod = (t.cuda() for t in (q, k, v, do))
+    o, lse = fa.fwd(qd, kd, vd, **gpu)
+    dq, dk, dv = fa.bwd(qd, kd, vd, o, lse, dod, **gpu)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status(None) == fa.FA_OK
+    args = dict(kw, scale=scale, slopes=sl, key_range=None)
+    q64, k64, v64, do64 = (t.double() for t in (q, k, v, do))
+    o_r, lse_r, av = ref.forward(q64, k64, v64, **args)
+    even = slice(0, N, 2)
+    A = scale * (q64.abs() @ k64.abs().mT).amax(-1) + (0.0 if sl is None else float(sl.max()) * N)
+    delta = (LARGE * A)[:, :, even]
+    o_, lse_ = o.double().cpu(), lse.double().cpu()
+    off = (lse_ - lse_r).abs()[:, :, even] - (delta + 6.25e-6 + 2.0 ** -20 * (1 + lse_r.abs()[:, :, even]))
+    assert bool((off <= 0).all()), float(off.max())
+    tol = 2.0 ** -8 * o_r.abs() + 2.0 ** -30
+    tol = tol[:, :, even] + (2.0 ** -7 + 2.0 ** -12 + 2 * delta[..., None]) * av[:, :, even]
+    assert bool(((o_ - o_r).abs()[:, :, even] <= tol).all())
+    exact, sums, more = ref.backward(q64, k64, v64, o_, lse_, do64, **args)
+    e, s, m = (t[0][:, :, even] for t in (exact, sums, more))
+    tol = 2.0 ** -8 * e.abs() + (2.0 ** -8 + 2.0 ** -12 + 2 * delta[..., None]) * s + 2.0 ** -18 * m + 2.0 ** -30
+    assert bool(((dq.double().cpu()[:, :, even] - e).abs() <= tol).all())
+    assert all(bool(torch.isfinite(t).all()) for t in (dk, dv))
+
+
+@pytest.mark.parametrize("d,N", [(128, 4193), (64, 1500), (256, 1500)])
+@pytest.mark.parametrize("slopes", [False, True])
+def test_large_cap_in_long_rows(d, N, slopes):
+    # key blocks whole and in parts, and sizes that a smaller cap with slopes gives 128-query steps
+    q, k, v, do = _draw(1, 1, 1, N, d, seed=d + N, q_std=2.0)
+    check(q, k, v, do, causal=True, softcap=1e5, slopes=_slopes(1) if slopes else None)
