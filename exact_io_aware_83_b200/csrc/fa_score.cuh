@@ -123,8 +123,8 @@ __device__ __forceinline__ void row_range(const ScoreCfg &c, int b, int i, int N
   }
   if (c.range) {
     const int2 r = c.range[static_cast<size_t>(b) * N + i];
-    lo = max(r.x, 0);
-    hi = min(r.y, N);
+    lo = min(max(r.x, 0), N);  // both into 0 .. N: users of lo and hi subtract key positions
+    hi = min(max(r.y, 0), N);
   }
   if (c.causal) hi = min(hi, i + 1);
 }

@@ -140,3 +140,22 @@ def test_large_cap_in_long_rows(d, N, slopes):
     # key blocks whole and in parts, and sizes that a smaller cap with slopes gives 128-query steps
     q, k, v, do = _draw(1, 1, 1, N, d, seed=d + N, q_std=2.0)
     check(q, k, v, do, causal=True, softcap=1e5, slopes=_slopes(1) if slopes else None)
+
+
+LOWEST, HIGHEST = -2 ** 31, 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("causal", [False, True])
+def test_range_bounds_at_the_ends_of_int32(d, causal):
+    # the bounds count as clamped to 0 .. N: rows that name no key by the lowest or the highest
+    # int32, beside rows that see keys and so bring in blocks beyond the first
+    N = 520
+    kinds = torch.tensor([(0, LOWEST), (HIGHEST, HIGHEST), (LOWEST, LOWEST), (LOWEST, HIGHEST), (LOWEST, 3), (500, HIGHEST),
+                          (HIGHEST, LOWEST), (0, 519), (130, LOWEST + 1), (HIGHEST - 1, 400)], dtype=torch.int64)
+    i = torch.arange(2 * N).view(2, N)
+    r = kinds[(i * 7 + i // 11) % len(kinds)].to(torch.int32)
+    q, k, v, do = _draw(2, 3, 1, N, d, seed=d + 17)
+    out = check(q, k, v, do, causal=causal, key_range=r)
+    none = (r[..., 1] <= 0) | (r[..., 0] >= N) | (r[..., 1] <= r[..., 0])
+    assert bool((out[0].cpu().transpose(1, 2)[none] == 0).all()) and bool((out[2].cpu().transpose(1, 2)[none] == 0).all())
