@@ -111,6 +111,7 @@ int check_score_args(float softcap, const float *slopes) {
 
 fa::ScoreCfg make_score(float softcap, const float *slopes, const int *key_range, int causal, float scale) {
   fa::ScoreCfg c{};
+  c.raw3 = c.raw5 = -1.f;
   if (softcap > 0.f) {
     c.cap_in = static_cast<float>(static_cast<double>(scale) / softcap);
     const double u = static_cast<double>(scale) / softcap, a = softcap * 1.4426950408889634;
@@ -121,13 +122,13 @@ fa::ScoreCfg make_score(float softcap, const float *slopes, const int *key_range
     constexpr double t3[4] = {0.9999994557708327, -0.33326317935183836, 0.13190296595162188, -0.044402225913669886};
     constexpr double t5[6] = {0.9999994135990478, -0.3332904237749518, 0.13281433872551196, -0.05160567377480486, 0.016743114805512608, -0.003067060223737072};
     auto fold = [&](const double *t, int deg, float *k) {
-      bool normal = true;
       double f = a * u;
       for (int i = 0; i <= deg; ++i, f *= u * u) {
-        k[i] = static_cast<float>(t[i] * f);
-        normal = normal && std::fabs(t[i] * f) > 0x1p-120 && std::fabs(t[i] * f) < 0x1p120;
+        const double x = t[i] * f;
+        if (!(std::fabs(x) > 0x1p-120 && std::fabs(x) < 0x1p120)) return false;
+        k[i] = static_cast<float>(x);
       }
-      return normal;
+      return true;
     };
     if (fold(t3, 3, c.k3)) c.raw3 = static_cast<float>(0.5 / u);
     if (fold(t5, 5, c.k5)) c.raw5 = static_cast<float>(1.0 / u);

@@ -35,8 +35,9 @@ namespace fa {
 struct ScoreCfg {
   float cap_in;         // scale / cap (0: no cap)
   float cap_log2;       // cap * log2(e)
-  // |q . k| up to which the folded polynomials of degree 3 and 5 hold (0: not used), and their
-  // coefficients: score in log2 units = r (k[0] + k[1] r^2 + k[2] r^4 + ...), r = q . k
+  // |q . k| up to which the folded polynomials of degree 3 and 5 hold (negative: not used, products
+  // of 0 included), and their coefficients: score in log2 units = r (k[0] + k[1] r^2 + k[2] r^4 +
+  // ...), r = q . k
   float raw3, raw5;
   float k3[4], k5[6];
   const float *slopes;  // [Hq] or nullptr

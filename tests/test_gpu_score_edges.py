@@ -159,3 +159,46 @@ def test_range_bounds_at_the_ends_of_int32(d, causal):
     out = check(q, k, v, do, causal=causal, key_range=r)
     none = (r[..., 1] <= 0) | (r[..., 0] >= N) | (r[..., 1] <= r[..., 0])
     assert bool((out[0].cpu().transpose(1, 2)[none] == 0).all()) and bool((out[2].cpu().transpose(1, 2)[none] == 0).all())
+
+
+def check_near_zero(q, k, v, do, causal, softcap):
+    """check, and in the gradients' bounds what a small cap makes of a score's error: the factor
+    1 - tanh^2(x / cap) is taken at an x that is off by up to delta = 2^-17 A, which for |x| near
+    delta or below may be anything between its values at |x| - delta and |x| + delta."""
+    o, lse = check(q, k, v, do, causal=causal, softcap=softcap, backward=False)
+    dev = [t.cuda() for t in (q, k, v)]
+    got = fa.bwd(*dev, o, lse, do.cuda(), causal=causal, softcap=softcap)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status(None) == fa.FA_OK
+    B, Hq, N, d = q.shape
+    g, scale = Hq // k.shape[1], 1 / math.sqrt(d)
+    args = dict(causal=causal, scale=scale, softcap=softcap, slopes=None, key_range=None)
+    q64, k64, v64, do64, o64, lse64 = (t.double().cpu() for t in (q, k, v, do, o, lse))
+    exact, sums, more = ref.backward(q64, k64, v64, o64, lse64, do64, **args)
+    kk, vv = k64.repeat_interleave(g, 1), v64.repeat_interleave(g, 1)
+    x = scale * (q64 @ kk.mT).abs()
+    delta = 2.0 ** -17 * scale * (q64.abs() @ kk.abs().mT).amax(-1, keepdim=True)
+    fac = lambda y: 1 - torch.tanh(y / softcap) ** 2
+    off = torch.maximum(fac((x - delta).clamp(min=0)) - fac(x), fac(x) - fac(x + delta))
+    p = torch.exp(ref.scores(q64, k64, causal, scale, softcap, None, None)[0] - lse64[..., None])
+    w = p * scale * off * ((do64 @ vv.mT).abs() + (do64 * o64).sum(-1, keepdim=True).abs())
+    heads = lambda t: t.view(B, -1, g, N, d).sum(2)
+    extra = (w @ kk.abs(), heads(w.mT @ q64.abs()), torch.zeros_like(v64))
+    for name, a, e, s, m, t in zip(("dQ", "dK", "dV"), got, exact, sums, more, extra):
+        a = a.double().cpu()
+        tol = (2.0 ** -8 * e.abs() + (2.0 ** -8 + 2.0 ** -12 + 2 * float(delta.max())) * s + 2.0 ** -18 * m
+               + 2.0 ** -30 + t)
+        assert bool(torch.isfinite(a).all()), name
+        assert bool(((a - e).abs() <= tol).all()), (name, float(((a - e).abs() / tol).max()))
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("softcap", [1e-9, 1e-6, 1e6])
+def test_rows_of_zero_scores(d, causal, softcap):
+    # whole warps of zero queries: all their scores are 0 at any cap, also one whose folded
+    # polynomial does not exist in fp32
+    q, k, v, do = _draw(1, 2, 1, 300, d, seed=d, q_std=2.0)
+    q[:, 0] = 0
+    q[:, 1, 64:256] = 0
+    check_near_zero(q, k, v, do, causal, softcap)
