@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <cstdio>
@@ -109,12 +110,20 @@ int check_score_args(float softcap, const float *slopes) {
   return FA_OK;
 }
 
+// Caps outside 2^-100 .. 2^100 count as the nearer end, so that 1 / cap, cap log2(e) and their
+// products stay finite: below, the scores are equal to fp32 either way; above, a cap changes no
+// score under 2^88 by more than its rounding.
+float usable_cap(float softcap) {
+  return softcap > 0.f ? std::fmin(std::fmax(softcap, 0x1p-100f), 0x1p100f) : softcap;
+}
+
 fa::ScoreCfg make_score(float softcap, const float *slopes, const int *key_range, int causal, float scale) {
   fa::ScoreCfg c{};
+  softcap = usable_cap(softcap);
   c.raw3 = c.raw5 = -1.f;
   if (softcap > 0.f) {
-    c.cap_in = static_cast<float>(static_cast<double>(scale) / softcap);
     const double u = static_cast<double>(scale) / softcap, a = softcap * 1.4426950408889634;
+    c.cap_in = static_cast<float>(std::fmin(u, FLT_MAX));
     c.cap_log2 = static_cast<float>(a);
     // tanh(u) / u as a polynomial of u^2: minimax fits on |u| <= 0.5 (degree 3, relative error
     // 5.4e-7) and |u| <= 1 (degree 5, 5.9e-7), with a and the powers of scale / cap folded in;
@@ -470,7 +479,7 @@ void fill_line(fa::LineParams &p, const void *q, void *o, float *lse, const int 
   p.causal = causal;
   p.scale = scale;
   p.sl2 = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634);
-  p.softcap = softcap;
+  p.softcap = usable_cap(softcap);
 }
 
 // Decode with changed scores: rows per K/V head up to which the pieces of fa_decode_score.cuh

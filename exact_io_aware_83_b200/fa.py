@@ -283,10 +283,16 @@ def fa_decode(q, k, v, o, lse, seqlens_k, workspace, workspace_bytes, B, Hq, Hkv
            "fa_decode")
 
 
+def _cap(softcap) -> float:
+    """A cap as C takes it: positive ones stay positive and finite in fp32."""
+    c = float(softcap)
+    return min(max(c, 2.0 ** -126), 2.0 ** 126) if 0.0 < c < math.inf else c
+
+
 def fa_fwd_score(q, k, v, o, lse, alibi_slopes, key_range, B, Hq, Hkv, N, d, causal, softcap, scale,
                  stream) -> None:
     _check(load().fa_fwd_score(q, k, v, o, lse, alibi_slopes, key_range, B, Hq, Hkv, N, d,
-                               int(causal), float(softcap), float(scale), stream), "fa_fwd_score")
+                               int(causal), _cap(softcap), float(scale), stream), "fa_fwd_score")
 
 
 def fa_bwd_score_workspace_bytes(B, Hq, Hkv, N, d) -> int:
@@ -297,7 +303,7 @@ def fa_bwd_score(q, k, v, o, lse, dout, dq, dk, dv, workspace, workspace_bytes, 
                  key_range, B, Hq, Hkv, N, d, causal, softcap, scale, stream) -> None:
     _check(load().fa_bwd_score(q, k, v, o, lse, dout, dq, dk, dv, workspace, workspace_bytes,
                                alibi_slopes, key_range, B, Hq, Hkv, N, d, int(causal),
-                               float(softcap), float(scale), stream), "fa_bwd_score")
+                               _cap(softcap), float(scale), stream), "fa_bwd_score")
 
 
 def fa_decode_score_num_splits(B, Hq, Hkv, Nq, Nk, d) -> int:
@@ -312,7 +318,7 @@ def fa_decode_score(q, k, v, o, lse, seqlens_k, alibi_slopes, workspace, workspa
                     Hkv, Nq, Nk, d, causal, num_splits, softcap, scale, stream) -> None:
     _check(load().fa_decode_score(q, k, v, o, lse, seqlens_k, alibi_slopes, workspace,
                                   workspace_bytes, B, Hq, Hkv, Nq, Nk, d, int(causal),
-                                  int(num_splits), float(softcap), float(scale), stream),
+                                  int(num_splits), _cap(softcap), float(scale), stream),
            "fa_decode_score")
 
 
@@ -341,7 +347,7 @@ def fa_decode_kv4(q, k_codes, k_params, v_codes, v_params, o, lse, seqlens_k, al
                   scale, stream) -> None:
     _check(load().fa_decode_kv4(q, k_codes, k_params, v_codes, v_params, o, lse, seqlens_k,
                                 alibi_slopes, workspace, workspace_bytes, B, Hq, Hkv, Nq, cap, d,
-                                int(causal), int(num_splits), float(softcap), float(scale),
+                                int(causal), int(num_splits), _cap(softcap), float(scale),
                                 stream), "fa_decode_kv4")
 
 

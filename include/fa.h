@@ -246,7 +246,8 @@ int fa_bwd_blocksparse(const void *q, const void *k, const void *v, const void *
  *     s_ij = softcap * tanh(x / softcap) - slope[h] * |i - j|,
  *     O_i = sum_j softmax_j(s_ij) v_j,  LSE_i = ln sum_j exp(s_ij)
  * over the keys lo_i <= j < hi_i (with causal = 1 also j <= i).
- *   softcap: 0 (scores as they are) or a finite c > 0.
+ *   softcap: 0 (scores as they are) or a finite c > 0 (below 2^-100 or above 2^100 it counts as
+ *        these).
  *   alibi_slopes: DEVICE fp32 [Hq] (4-byte aligned), or NULL for no bias.
  *   key_range: DEVICE int32 [B, N, 2] (8-byte aligned), (lo_i, hi_i) of every query row of a
  *        batch entry, the same for all heads, or NULL for 0, N; values are clamped to 0 .. N.

@@ -202,3 +202,34 @@ def test_rows_of_zero_scores(d, causal, softcap):
     q[:, 0] = 0
     q[:, 1, 64:256] = 0
     check_near_zero(q, k, v, do, causal, softcap)
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("softcap", [1e-45, 1e-42, 1e-37, 1e-25, 1e25, 1e37, 3.4e38])
+def test_caps_at_the_ends_of_fp32(d, softcap):
+    # scores all but equal, or all but uncapped; zero rows among them
+    N = 300
+    q, k, v, do = _draw(1, 2, 1, N, d, seed=d, q_std=2.0)
+    q[:, 0, 3:7] = 0
+    q[:, 1, 128:192] = 0
+    check_near_zero(q, k, v, do, True, softcap)
+    for Nq in (1, 10):
+        lens, scale = [N], 1 / math.sqrt(d)
+        rows = q[:, :, :Nq].contiguous()
+        o_r, lse_r, av, size = _decode_ref(rows, k, v, lens, True, scale, softcap, None)
+        o, lse = fa.decode(rows.cuda(), k.cuda(), v.cuda(), causal=True, softcap=softcap)
+        tol = 2.0 ** -8 * np.abs(o_r) + (2.0 ** -6.9 + 2 * LARGE * size[..., None]) * av + 2.0 ** -30
+        assert (np.abs(_f64(o) - o_r) <= tol).all()
+        assert (np.abs(_f64(lse) - lse_r) <= LARGE * size + 2.0 ** -20 * (1 + np.abs(lse_r))).all()
+        pk, pv = kv4_reference.quantise(_f64(k)), kv4_reference.quantise(_f64(v))
+        k64, v64 = kv4_reference.values(*pk), kv4_reference.values(*pv)
+        o_r, lse_r, av, _ = kv4_reference.decode(_f64(rows), k64, v64, lens, True, scale, softcap)
+        big = np.repeat(np.abs(pk[2]) + 15 * pk[1], 32, -1)
+        delta = LARGE * scale * np.einsum("bhtc,bhc->bht", np.abs(_f64(rows)), np.repeat(big.max(2), 2, 1)) + 2.0 ** -20
+        o, lse = fa.decode_kv4(rows.cuda(), _cache_of(k, v, 320), softcap=softcap, causal=True,
+                               seqlens_k=torch.tensor(lens, dtype=torch.int32, device="cuda"))
+        tol = (2.0 ** -8 * np.abs(o_r) + (2.0 ** -10 + 2 * delta[..., None] + 2.0 ** -18) * av
+               + 2.0 ** -24 * np.abs(v64).max())
+        assert (np.abs(_f64(o) - o_r) <= tol).all()
+        assert (np.abs(_f64(lse) - lse_r) <= delta + 2.0 ** -20 * (1 + np.abs(lse_r))).all()
+    assert fa.fa_device_status(None) == fa.FA_OK
