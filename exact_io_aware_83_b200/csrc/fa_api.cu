@@ -1030,9 +1030,9 @@ int fa_device_status(void *stream) {
     if (cudaMemcpyToSymbol(fa::g_fa_status, &zero, sizeof(int)) != cudaSuccess ||
         cudaMemcpyToSymbol(fa::g_fa_status_site, &zero64, sizeof(zero64)) != cudaSuccess)
       return FA_ERR_CUDA;
+    return status;  // the other unit's word keeps its error, if any, for the next call
   }
-  const int score = fa_host::take_score_status();
-  return status != FA_OK ? status : score;
+  return fa_host::take_score_status();
 }
 
 }  // extern "C"

@@ -5,6 +5,7 @@
 #include <cuda.h>
 #include <cuda_runtime.h>
 
+#include <atomic>
 #include <cfloat>
 #include <cmath>
 #include <cstdint>
@@ -30,6 +31,7 @@ using namespace fa_host;
 struct ScoreState {
   std::once_flag once;
   bool ok = false;
+  std::atomic<bool> ready{false};  // ok, for readers outside of call_once
 };
 ScoreState g_score_dev[kMaxDevices];
 
@@ -98,6 +100,7 @@ bool score_ready() {
     ok = ok && set_smem(fa::fa_decode_score_kernel<128, 2>, fa::DecScoreLayout<128, 2>::kSmemBytes);
     ok = ok && set_smem(fa::fa_decode_score_kernel<256, 1>, fa::DecScoreLayout<256, 1>::kSmemBytes);
     st.ok = ok;
+    st.ready.store(ok);
   });
   return st.ok;
 }
@@ -509,7 +512,9 @@ void launch_kv4(const fa::KV4DecodeParams &p, cudaStream_t s) {
 
 namespace fa_host {
 int take_score_status() {
-  int status = 0;
+  int status = 0, dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return FA_ERR_CUDA;
+  if (dev < 0 || dev >= kMaxDevices || !g_score_dev[dev].ready.load()) return FA_OK;  // no kernel of this unit has run
   if (cudaMemcpyFromSymbol(&status, fa::g_fa_status, sizeof(int)) != cudaSuccess) return FA_ERR_CUDA;
   if (status != FA_OK) {
     const int zero = 0;

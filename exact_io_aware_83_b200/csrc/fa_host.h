@@ -35,7 +35,7 @@ constexpr int kMaxDecodeSplits = 1024;
 constexpr int kMaxDevices = 64;
 
 // Defined in fa_api_score.cu: the status word of its kernels on the current device, cleared
-// when it is not FA_OK.
+// when it is not FA_OK (FA_OK without a look at the device before the first of them).
 int take_score_status();
 
 // A kernel that rebalances registers with setmaxnreg must have been compiled for the launch

@@ -448,7 +448,9 @@ int fa_merge(const float *o_parts, const float *lse_parts, void *o, float *lse, 
 
 /*
  * Synchronises `stream`, returns the device status of the current device
- * (FA_OK, FA_ERR_DEVICE_TIMEOUT or FA_ERR_SEQLENS) and clears it.  Returns FA_ERR_CUDA if the
+ * (FA_OK, FA_ERR_DEVICE_TIMEOUT or FA_ERR_SEQLENS) and clears it.  The kernels for plain scores
+ * and those for changed scores and the 4-bit cache keep their first error each; when both have
+ * one, this call returns the former's and the next call the latter's.  Returns FA_ERR_CUDA if the
  * synchronisation itself fails.
  */
 int fa_device_status(void *stream);

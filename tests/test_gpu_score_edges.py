@@ -233,3 +233,20 @@ def test_caps_at_the_ends_of_fp32(d, softcap):
         assert (np.abs(_f64(o) - o_r) <= tol).all()
         assert (np.abs(_f64(lse) - lse_r) <= delta + 2.0 ** -20 * (1 + np.abs(lse_r))).all()
     assert fa.fa_device_status(None) == fa.FA_OK
+
+
+def test_status_reports_one_error_of_each_kind():
+    # a wait that ran out and a position outside a cache: both are reported, one per call
+    cache = fa.kv4_alloc(1, 1, 64, 64)
+    x = torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16, device="cuda")
+    outside = torch.full((1,), 64, dtype=torch.int32, device="cuda")
+    assert fa.fa_device_status(None) == fa.FA_OK
+    fa.kv4_write(cache, x, x, start=outside)
+    assert fa.load().fa_watchdog_selftest(1000, None) == fa.FA_OK
+    got = [fa.fa_device_status(None) for _ in range(3)]
+    assert sorted(got) == [fa.FA_OK, fa.FA_ERR_DEVICE_TIMEOUT, fa.FA_ERR_SEQLENS] and got[2] == fa.FA_OK, got
+    # two of the same kind are one error
+    for _ in range(2):
+        fa.kv4_write(cache, x, x, start=outside)
+    assert fa.fa_device_status(None) == fa.FA_ERR_SEQLENS
+    assert fa.fa_device_status(None) == fa.FA_OK
