@@ -250,3 +250,29 @@ def test_status_reports_one_error_of_each_kind():
         fa.kv4_write(cache, x, x, start=outside)
     assert fa.fa_device_status(None) == fa.FA_ERR_SEQLENS
     assert fa.fa_device_status(None) == fa.FA_OK
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+@pytest.mark.parametrize("splits", [1, 2, 3, 60, 148, 1024])
+def test_decode_of_long_caches_in_few_and_many_pieces(d, splits):
+    # pieces of dozens of blocks, which refill every stage of the ring many times, and heads that
+    # dozens of pieces share; keys and values behind the last one are NaN.  P keeps 16 bits here:
+    # bounds of test_decode_with_caps_above_every_score, the distance off by 2^-22 of its largest.
+    B, Hq, Hkv, Nq, Nk, lens, scale = 3, 6, 2, 2, 9000, [8999, 17, 4352], 1 / math.sqrt(d)
+    g = torch.Generator().manual_seed(d + splits)
+    q = (torch.randn(B, Hq, Nq, d, generator=g) * 3).to(torch.bfloat16)
+    k, v = (torch.randn(B, Hkv, Nk, d, generator=g).to(torch.bfloat16) for _ in range(2))
+    for b in range(B):
+        k[b, :, lens[b]:], v[b, :, lens[b]:] = float("nan"), float("nan")
+    slopes = torch.tensor([2.0 ** -(8 + h) for h in range(Hq)])
+    o, lse = fa.decode(q.cuda(), k.cuda(), v.cuda(), seqlens_k=torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                       causal=True, softcap=20.0, alibi_slopes=slopes.cuda(), num_splits=splits)
+    torch.cuda.synchronize()
+    assert fa.fa_device_status(None) == fa.FA_OK
+    o_r, lse_r, av, size = _decode_ref(q, k, v, lens, True, scale, 20.0, slopes)
+    delta = LARGE * size + 2.0 ** -22 * float(slopes.max()) * Nk
+    tol = 2.0 ** -8 * np.abs(o_r) + (2.0 ** -14 + 2 * delta[..., None]) * av + 2.0 ** -30
+    if splits < 60:  # a warp's accumulator takes 2 * 9000 / 64 products: 2^-22 of the running sum each
+        tol += 2.0 ** -14 * av
+    assert (np.abs(_f64(o) - o_r) <= tol).all(), float((np.abs(_f64(o) - o_r) / tol).max())
+    assert (np.abs(_f64(lse) - lse_r) <= delta + 2.0 ** -20 * (1 + np.abs(lse_r))).all()
