@@ -254,8 +254,9 @@ int fa_bwd_blocksparse(const void *q, const void *k, const void *v, const void *
  *        Packed documents, visible prefixes, padding and windows are such ranges, and so is
  *        what several of them leave.  A row with hi <= lo gets O = 0 and LSE = -inf.
  *   q, k, v, o, lse, B, Hq, Hkv, N, d, causal, scale, stream: as fa_fwd.
- * Key blocks (of 128, 64 for d = 256) that lie outside the ranges of all 128 rows of a query
- * block are neither loaded nor multiplied.  Every row of K and V must hold finite values,
+ * A block of 128 query rows multiplies the key blocks (of 128, 64 for d = 256) from the smallest lo
+ * to the largest hi of its rows; key blocks that no row of the CTA's one or two query blocks
+ * brings in this way are not loaded.  Every row of K and V must hold finite values,
  * also those that no query sees (0 * NaN is NaN in the products).
  */
 int fa_fwd_score(const void *q, const void *k, const void *v, void *o, float *lse,
@@ -346,7 +347,8 @@ int fa_decode(const void *q, const void *k, const void *v, void *o, float *lse,
 /*
  * fa_decode with changed scores (softcap and alibi_slopes as for fa_fwd_score; the distance of
  * new row t and key j is |seqlens_k[b] - Nq + t - j|).  Rows of the cache behind the last
- * valid key may hold anything.
+ * valid key may hold anything; valid ones must be finite, also those that the causal mask hides
+ * from some of the new rows (0 * NaN is NaN).  There is no key range: the valid keys start at 0.
  *   num_splits: 1 .. 1024.  With up to 16 rows (Hq / Hkv) * Nq per K/V head (8 for d = 256),
  *        the blocks of valid keys of all batch entries and heads are laid end to end and cut
  *        into num_splits equal pieces, one CTA each, so that lengths that differ leave no SM
@@ -423,7 +425,10 @@ int fa_kv4_read(const void *k_codes, const void *k_params, const void *v_codes,
  *        second kernel.  fa_decode_kv4_num_splits gives the library's choice.
  *   workspace: device scratch of fa_decode_kv4_workspace_bytes() bytes, 16-byte aligned (may
  *        be NULL when that is 0, i.e. num_splits == 1).
- * Limit: (Hq / Hkv) * Nq <= 128.
+ * Valid tokens must be finite as for fa_decode_score, and start at 0 (no key range).
+ * Limit: (Hq / Hkv) * Nq <= 128 rows per K/V head.  They are taken 8 at a time (16 with more than
+ * 8 rows and d = 64 or 128), and each time reads the head's part of the cache: with two such
+ * tiles and more, fa_decode over a bf16 cache can be the faster one when the caches exceed L2.
  */
 int fa_decode_kv4(const void *q, const void *k_codes, const void *k_params, const void *v_codes,
                   const void *v_params, void *o, float *lse, const int *seqlens_k,
